@@ -6,7 +6,8 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = ["moonep_api.hip", "moonep_plan.hip", "moonep_move.hip"]
+SOURCES = ["moonep_api.hip", "moonep_plan.hip", "moonep_move.hip", "moonep_ffn.hip",
+           "moonep_norm.hip"]
 STREAM_SOURCES = ["moonep_streams.hip"]
 
 HIPCC_FLAGS = [

@@ -10,15 +10,6 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int check_desc(const moonep_plan_desc* d) {
-  if (!d || d->magic != kMagic || !d->dev) return MOONEP_EPLAN;
-  moonep_sizes s;
-  if (fill_sizes(d->sz.R, d->sz.E, d->sz.K, d->sz.S, d->sz.slots, &s) != MOONEP_OK)
-    return MOONEP_EPLAN;
-  if (std::memcmp(&s, &d->sz, sizeof(s)) != 0) return MOONEP_EPLAN;
-  return MOONEP_OK;
-}
-
 // hipGetLastError() returns, and clears, the last error of the calling thread, whichever
 // call caused it.  Each entry point clears it right before its launches, so the status it
 // reads afterwards belongs to its own launches only.

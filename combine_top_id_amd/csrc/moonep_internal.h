@@ -5,6 +5,7 @@
 
 #include <stdint.h>
 #include <algorithm>
+#include <cstring>
 #include <hip/hip_runtime.h>
 
 #include "moonep.h"
@@ -88,6 +89,16 @@ inline int fill_sizes(int R, int E, int K, int S, int slots, moonep_sizes* s) {
   s->workspace_bytes = (kWsCtl + align64((int64_t)s->nblk * E) + align64(s->nblk) +
                         align64((int64_t)s->nblk * kMapWaves * E) +
                         align64((int64_t)s->nblk * kMapWaves * (Q - 1) * E)) * 4;
+  return MOONEP_OK;
+}
+
+// A plan descriptor as a call is given it: filled by a plan call and not changed since.
+inline int check_desc(const moonep_plan_desc* d) {
+  if (!d || d->magic != kMagic || !d->dev) return MOONEP_EPLAN;
+  moonep_sizes s;
+  if (fill_sizes(d->sz.R, d->sz.E, d->sz.K, d->sz.S, d->sz.slots, &s) != MOONEP_OK)
+    return MOONEP_EPLAN;
+  if (std::memcmp(&s, &d->sz, sizeof(s)) != 0) return MOONEP_EPLAN;
   return MOONEP_OK;
 }
 

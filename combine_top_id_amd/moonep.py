@@ -68,6 +68,18 @@ def lib():
     L.moonep_combine_staged.argtypes = [ctypes.POINTER(PlanDesc), vp, i32, vp, vp, vp]
     L.moonep_prefetch_weight.argtypes = [ctypes.POINTER(PlanDesc), vp, i64, vp, vp]
     L.moonep_expert_stub.argtypes = [ctypes.POINTER(PlanDesc), vp, vp, vp, vp, i64, i32, vp, vp]
+    PD, f32 = ctypes.POINTER(PlanDesc), ctypes.c_float
+    L.moonep_expert_ffn.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp, vp]
+    L.moonep_expert_ffn_bwd_data.argtypes = [PD, vp, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp]
+    L.moonep_expert_ffn_bwd_weight.argtypes = [PD, vp, vp, vp, vp, i32, i32, vp, vp, i64, i32, vp]
+    L.moonep_rmsnorm.argtypes = [vp, vp, vp, f32, i64, i32, vp, vp, vp, vp]
+    L.moonep_rmsnorm_q8.argtypes = [vp, vp, vp, f32, i64, i32, vp, vp, vp, vp]
+    L.moonep_q8_unpack.argtypes = [vp, i64, i32, vp, vp]
+    L.moonep_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp]
+    L.moonep_q8_row_bytes.argtypes = [i32]
+    L.moonep_rmsnorm_bwd_workspace.argtypes = [i64, i32]
+    for f in ("moonep_q8_row_bytes", "moonep_rmsnorm_bwd_workspace"):
+        getattr(L, f).restype = i64
     L.moonep_plan_status.argtypes = [ctypes.POINTER(PlanDesc), ctypes.POINTER(PlanStats), vp]
     L.moonep_strerror.argtypes = [i32]
     L.moonep_strerror.restype = ctypes.c_char_p
@@ -75,7 +87,9 @@ def lib():
               "moonep_combine",
               "moonep_reduce_grad", "moonep_plan_status", "moonep_dispatch_bwd",
               "moonep_combine_bwd", "moonep_prefetch_weight", "moonep_expert_stub",
-              "moonep_dispatch_staged", "moonep_combine_staged"):
+              "moonep_dispatch_staged", "moonep_combine_staged", "moonep_expert_ffn",
+              "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_rmsnorm",
+              "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -85,7 +99,12 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
            "moonep_combine",
            "moonep_reduce_grad", "moonep_plan_status", "moonep_strerror",
            "moonep_dispatch_bwd", "moonep_combine_bwd", "moonep_prefetch_weight",
-           "moonep_expert_stub", "moonep_dispatch_staged", "moonep_combine_staged")
+           "moonep_expert_stub", "moonep_dispatch_staged", "moonep_combine_staged",
+           "moonep_expert_ffn", "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight",
+           "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
+           "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd")
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 
 def _check(rc):
@@ -362,6 +381,201 @@ def moonep_reduce_grad(plan: Plan, home_grad, rep_grad, stream=None):
                                     _dev(home_grad, torch.float32, "home_grad", D), rep_p, G_el,
                                     _stream(stream, D)))
     return home_grad
+
+
+def _bytes(n):
+    """The result of a host-only size call: bytes, or a negative error code."""
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def _rows(t, dtype, name, rows, cols, device, like):
+    """`t` checked to be [rows, cols] (its device pointer comes second), allocated next to
+    `like` if it is None."""
+    if t is None:
+        t = torch.empty(rows, cols, dtype=dtype, device=like.device)
+    p = _dev(t, dtype, name, device)
+    if t.numel() != rows * cols:
+        raise MoonepError(f"{name} must be [{rows}, {cols}]")
+    return t, p
+
+
+def _slabs(plan, home, slot, el, dtype, names):
+    """Device pointers and the pitch of an [E, pitch] and an [R, slots, pitch] array of
+    experts' slabs of at least `el` elements."""
+    D = plan.blob.device
+    pitch = home.shape[-1]
+    if home.numel() != plan.sz.E * pitch or pitch < el:
+        raise MoonepError(f"{names[0]} must be [E, 3*I*H or more]")
+    hp = _dev(home, dtype, names[0], D)
+    n = plan.sz.R * plan.sz.slots * pitch
+    if (slot.numel() if slot is not None else 0) != n:
+        raise MoonepError(f"{names[1]} must be [R, slots, {pitch}]")
+    return hp, (_dev(slot, dtype, names[1], D) if n else ctypes.c_void_p(0)), pitch
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise MoonepError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=False, h=None, gu=None,
+                      y=None, stream=None):
+    """The gated feed-forward experts: y[row] = Wd (act(Wg x) * (Wu x)) with x = recv[row] and
+    the weights of the row's group.  recv bf16 [R*NvS, H]; home_w bf16 [E, W_el], an
+    expert's slab being gate [I, H], up [I, H], down [H, I]; slot_w bf16 [R, slots, W_el].
+    Returns (y, h, gu): y bf16 [R*NvS, H], h bf16 [R*NvS, I], and, where `save` is true or
+    a buffer is passed, the gate and up rows gu bf16 [R*NvS, 2*I] (else None).  The
+    gradients need h and gu."""
+    D, n = plan.blob.device, plan.sz.recv_rows
+    H = recv.shape[-1]
+    _, rp = _rows(recv, torch.bfloat16, "recv", n, H, D, recv)
+    wp, sp, W_el = _slabs(plan, home_w, slot_w, 3 * I * H, torch.bfloat16, ("home_w", "slot_w"))
+    h, hp = _rows(h, torch.bfloat16, "h", n, I, D, recv)
+    y, yp = _rows(y, torch.bfloat16, "y", n, H, D, recv)
+    gp = ctypes.c_void_p(0)
+    if save or gu is not None:
+        gu, gp = _rows(gu, torch.bfloat16, "gu", n, 2 * I, D, recv)
+    _check(lib().moonep_expert_ffn(ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, W_el, gp, hp,
+                                   yp, _stream(stream, D)))
+    return y, h, gu
+
+
+def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu", g_gu=None,
+                               g_recv=None, stream=None):
+    """Gradient of moonep_expert_ffn with respect to the rows, from g_y bf16 [R*NvS, H] and the
+    saved gu.  Returns (g_recv bf16 [R*NvS, H], g_gu bf16 [R*NvS, 2*I]); g_gu may be gu."""
+    D, n = plan.blob.device, plan.sz.recv_rows
+    H = g_y.shape[-1]
+    _, yp = _rows(g_y, torch.bfloat16, "g_y", n, H, D, g_y)
+    _, gp = _rows(gu, torch.bfloat16, "gu", n, 2 * I, D, g_y) if gu is not None else (None, None)
+    if gp is None:
+        raise MoonepError("gu must be a GPU tensor")
+    wp, sp, W_el = _slabs(plan, home_w, slot_w, 3 * I * H, torch.bfloat16, ("home_w", "slot_w"))
+    g_gu, ggp = _rows(g_gu, torch.bfloat16, "g_gu", n, 2 * I, D, g_y)
+    g_recv, grp = _rows(g_recv, torch.bfloat16, "g_recv", n, H, D, g_y)
+    _check(lib().moonep_expert_ffn_bwd_data(ctypes.byref(plan.desc), yp, gp, H, I, _act(act), wp, sp,
+                                            W_el, ggp, grp, _stream(stream, D)))
+    return g_recv, g_gu
+
+
+def moonep_expert_ffn_bwd_weight(plan: Plan, recv, g_y, h, g_gu, home_grad=None, rep_grad=None,
+                                 accumulate=False, stream=None):
+    """Gradient of moonep_expert_ffn with respect to the weights: home_grad fp32 [E, G_el]
+    (overwritten, or added to with `accumulate`) and rep_grad fp32 [R, slots, G_el]
+    (overwritten in the slots the plan uses), laid out as the weights' slabs;
+    moonep_reduce_grad then adds the replicas to their homes.  Returns both."""
+    D, n = plan.blob.device, plan.sz.recv_rows
+    if h is None or g_y is None or g_gu is None:
+        raise MoonepError("g_y, h and g_gu must be GPU tensors")
+    H, I = recv.shape[-1], h.shape[-1]
+    _, rp = _rows(recv, torch.bfloat16, "recv", n, H, D, recv)
+    _, yp = _rows(g_y, torch.bfloat16, "g_y", n, H, D, recv)
+    _, hp = _rows(h, torch.bfloat16, "h", n, I, D, recv)
+    _, gp = _rows(g_gu, torch.bfloat16, "g_gu", n, 2 * I, D, recv)
+    if home_grad is None:
+        if accumulate:
+            raise MoonepError("accumulate needs a home_grad to add to")
+        home_grad = torch.empty(plan.sz.E, 3 * I * H, dtype=torch.float32, device=recv.device)
+    if rep_grad is None:
+        rep_grad = torch.empty(plan.sz.R, plan.sz.slots, home_grad.shape[-1], dtype=torch.float32,
+                               device=recv.device)
+    wp, sp, G_el = _slabs(plan, home_grad, rep_grad, 3 * I * H, torch.float32, ("home_grad", "rep_grad"))
+    _check(lib().moonep_expert_ffn_bwd_weight(ctypes.byref(plan.desc), rp, yp, hp, gp, H, I, wp, sp, G_el,
+                                              int(bool(accumulate)), _stream(stream, D)))
+    return home_grad, rep_grad
+
+
+def _norm_args(x, gamma, res, h, rstd, stats):
+    """The checked arguments that the norm's two forms share."""
+    xp = _dev(x, torch.bfloat16, "x")
+    D, H = x.device, x.shape[-1]
+    T = x.numel() // H if H else 0
+    none = ctypes.c_void_p(0)
+    gp = _dev(gamma, torch.bfloat16, "gamma", D)
+    if gamma.numel() != H:
+        raise MoonepError("gamma must be [H]")
+    rp = _rows(res, torch.bfloat16, "res", T, H, D, x)[1] if res is not None else none
+    if h is not None or res is not None:
+        h, hp = _rows(h, torch.bfloat16, "h", T, H, D, x)
+    else:
+        h, hp = x, none                  # without a residual the stream is x itself
+    sp = none
+    if stats or rstd is not None:
+        if rstd is None:
+            rstd = torch.empty(T, dtype=torch.float32, device=D)
+        sp = _dev(rstd, torch.float32, "rstd", D)
+        if rstd.numel() != T:
+            raise MoonepError("rstd must be [T]")
+    return D, T, H, xp, rp, gp, h, hp, rstd, sp
+
+
+def moonep_rmsnorm(x, gamma, eps=1e-6, res=None, out=None, h=None, rstd=None, stats=True, stream=None):
+    """h = bf16(x + res), out = bf16(h * rstd * gamma), rstd = 1 / sqrt(mean(h^2) + eps), row by
+    row.  x, res bf16 [T, H], gamma bf16 [H].  Returns (out, h, rstd): h is x where there is
+    no residual and no buffer for it, rstd (fp32 [T]) is None where `stats` is false."""
+    D, T, H, xp, rp, gp, h, hp, rstd, sp = _norm_args(x, gamma, res, h, rstd, stats)
+    if out is None:
+        out = torch.empty_like(x)
+    op = _rows(out, torch.bfloat16, "out", T, H, D, x)[1]
+    _check(lib().moonep_rmsnorm(xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D)))
+    return out, h, rstd
+
+
+def moonep_q8_row_bytes(H):
+    """Bytes of a row of H elements in 8 bits: codes, a scale for 32 of them, padding to 16."""
+    return _bytes(lib().moonep_q8_row_bytes(H))
+
+
+def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None, stats=True, stream=None):
+    """moonep_rmsnorm with its output as 8-bit rows, uint8 [T, moonep_q8_row_bytes(H)].
+    `rows.view(torch.bfloat16)` is what moonep_dispatch moves.  Returns (rows, h, rstd)."""
+    D, T, H, xp, rp, gp, h, hp, rstd, sp = _norm_args(x, gamma, res, h, rstd, stats)
+    rows, op = _rows(rows, torch.uint8, "rows", T, moonep_q8_row_bytes(H), D, x)
+    _check(lib().moonep_rmsnorm_q8(xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D)))
+    return rows, h, rstd
+
+
+def moonep_q8_unpack(rows, H, out=None, stream=None):
+    """8-bit rows (uint8 [N, moonep_q8_row_bytes(H)], or the same bytes as bf16 elements, as the
+    dispatch returns them) expanded to bf16 [N, H]."""
+    rb = moonep_q8_row_bytes(H)
+    if isinstance(rows, torch.Tensor) and rows.dtype == torch.bfloat16 and rows.is_contiguous():
+        rows = rows.view(torch.uint8)
+    rp = _dev(rows, torch.uint8, "rows")
+    if rows.numel() % rb:
+        raise MoonepError(f"rows must be [N, {rb}] bytes")
+    N, D = rows.numel() // rb, rows.device
+    out, op = _rows(out, torch.bfloat16, "out", N, H, D, rows)
+    _check(lib().moonep_q8_unpack(rp, N, H, op, _stream(stream, D)))
+    return out
+
+
+def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, workspace=None, stream=None):
+    """Backward of the norm from the stored h bf16 [T, H] and rstd fp32 [T]; g_h, if given, is
+    the gradient that reaches h past the norm.  Returns (g_x bf16 [T, H], the gradient of x
+    and of res; g_gamma fp32 [H])."""
+    op = _dev(g_out, torch.bfloat16, "g_out")
+    D, H = g_out.device, g_out.shape[-1]
+    T = g_out.numel() // H if H else 0
+    _, hp = _rows(h, torch.bfloat16, "h", T, H, D, g_out)
+    gp = _dev(gamma, torch.bfloat16, "gamma", D)
+    sp = _dev(rstd, torch.float32, "rstd", D)
+    if gamma.numel() != H or rstd.numel() != T:
+        raise MoonepError("gamma must be [H] and rstd [T]")
+    ghp = _rows(g_h, torch.bfloat16, "g_h", T, H, D, g_out)[1] if g_h is not None else ctypes.c_void_p(0)
+    g_x, xp = _rows(g_x, torch.bfloat16, "g_x", T, H, D, g_out)
+    g_gamma, ggp = _rows(g_gamma, torch.float32, "g_gamma", 1, H, D, g_out)
+    need = _bytes(lib().moonep_rmsnorm_bwd_workspace(T, H))
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=D)
+    wp = _dev(workspace, torch.uint8, "workspace", D)
+    if workspace.numel() < need:
+        raise MoonepError(f"workspace must hold {need} bytes")
+    _check(lib().moonep_rmsnorm_bwd(op, hp, gp, sp, ghp, T, H, wp, xp, ggp, _stream(stream, D)))
+    return g_x, g_gamma.view(H)
 
 
 def moonep_plan_status(plan: Plan, stream=None) -> dict:

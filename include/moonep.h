@@ -50,6 +50,10 @@ extern "C" {
 #define MOONEP_MAX_E 1024
 #define MOONEP_MAX_K 32
 #define MOONEP_MAX_SLOTS 256
+#define MOONEP_MAX_FFN 32768     /* hidden and intermediate sizes of an expert          */
+#define MOONEP_MAX_NORM 32768    /* hidden size of a normed row                         */
+#define MOONEP_ACT_SILU 0        /* z / (1 + e^-z)                                      */
+#define MOONEP_ACT_GELU 1        /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2     */
 /* largest planning workspace moonep_plan_noalloc serves from its static device array */
 #define MOONEP_NOALLOC_WORKSPACE_MAX (8 << 20)
 
@@ -257,6 +261,113 @@ int moonep_prefetch_weight(const moonep_plan_desc* plan, const uint16_t* home_w,
 int moonep_expert_stub(const moonep_plan_desc* plan, const int32_t* topk_ids,
                        const uint16_t* recv, const uint16_t* home_w, const uint16_t* slot_w,
                        int64_t W_el, int H, uint16_t* y, hipStream_t stream);
+
+/* The gated feed-forward experts, the expert compute between dispatch and combine ("MoonshotAI/MoonEP
+ * 딥다이브", section 1: dispatch -> expert compute -> combine; section 2, point 2: the
+ * receive buffer is handed to expert compute as a view).  For every mapped row:
+ *   gate = Wg x, up = Wu x, h = act(gate) * up        (one kernel; fp32 sums, h rounded to bf16 once)
+ *   y = Wd h                                          (fp32 sums, rounded to bf16 once)
+ * with the weights the row's group uses: home_w[e] for a home group, slot_w[r, slot] for a
+ * slot group and home_w[e] (read across partitions) for a fallback piece.
+ *   recv    device bf16 [R*NvS, H]
+ *   home_w  device bf16 [E, W_el]: an expert's slab is its gate [I, H], up [I, H] and down
+ *           [H, I] matrices, row-major, in this order; W_el >= 3*I*H is the slabs' pitch
+ *   slot_w  device bf16 [R, slots, W_el] (moonep_prefetch_weight's)
+ *   act     MOONEP_ACT_SILU or MOONEP_ACT_GELU
+ *   gu      device bf16 [R*NvS, 2*I] or NULL: gate, then up, of every row, for the backward pass
+ *   h       device bf16 [R*NvS, I]: scratch of an inference call; the weights' gradient reads it
+ *   y       device bf16 [R*NvS, H]
+ * H and I are multiples of 8, at most MOONEP_MAX_FFN, W_el a multiple of 8; all pointers
+ * 16-byte aligned.  Padding rows of recv are not read and those of gu, h and y not written.
+ * No output may overlap an input or another output.  EHIP can follow the first of the two
+ * launches.  Deterministic. */
+int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H, int I, int act,
+                      const uint16_t* home_w, const uint16_t* slot_w, int64_t W_el, uint16_t* gu,
+                      uint16_t* h, uint16_t* y, hipStream_t stream);
+
+/* Gradient of moonep_expert_ffn with respect to the rows, reusing the forward plan (deep
+ * dive, section 4, design pattern 1).  For every mapped row:
+ *   g_h = Wd^T g_y;  g_gate = g_h * up * act'(gate),  g_up = g_h * act(gate)
+ *   g_recv = Wg^T g_gate + Wu^T g_up
+ * from the saved gate and up of `gu`; fp32 sums, g_gate and g_up rounded to bf16 (they are
+ * an output, and the second product's input), g_recv rounded to bf16 once.
+ *   g_y     device bf16 [R*NvS, H]      gu      device bf16 [R*NvS, 2*I]
+ *   g_gu    device bf16 [R*NvS, 2*I], may be gu itself (in place)
+ *   g_recv  device bf16 [R*NvS, H]
+ * Weights, sizes, padding rows and errors as in moonep_expert_ffn. */
+int moonep_expert_ffn_bwd_data(const moonep_plan_desc* plan, const uint16_t* g_y,
+                               const uint16_t* gu, int H, int I, int act, const uint16_t* home_w,
+                               const uint16_t* slot_w, int64_t W_el, uint16_t* g_gu,
+                               uint16_t* g_recv, hipStream_t stream);
+
+/* Gradient of moonep_expert_ffn with respect to the weights, kept apart for each replica
+ * until moonep_reduce_grad adds it to its home (deep dive, section 4, design pattern 3):
+ *   gate, up: sum over rows of g_gu[row, :]^T recv[row, :];  down: of g_y[row, :]^T h[row, :]
+ * in fp32, over the rows of the group.  home_grad[e] takes expert e's home group and its
+ * fallback pieces, which own no slot; rep_grad[r, slot] takes a slot's group.
+ *   recv, g_y  device bf16 [R*NvS, H]     h  device bf16 [R*NvS, I]
+ *   g_gu       device bf16 [R*NvS, 2*I]   (moonep_expert_ffn_bwd_data's)
+ *   home_grad  device fp32 [E, G_el], laid out as the slabs of home_w; G_el >= 3*I*H
+ *   rep_grad   device fp32 [R, slots, G_el]; slots no piece uses are not written
+ *   accumulate 0: home_grad is overwritten (with zeros for an expert without rows);
+ *              1: the sums are added to it.  rep_grad is overwritten either way.
+ * Of a slab, the first 3*I*H elements are written.  H and I multiples of 8, G_el of 4; all
+ * pointers 16-byte aligned.  Deterministic. */
+int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* recv,
+                                 const uint16_t* g_y, const uint16_t* h, const uint16_t* g_gu,
+                                 int H, int I, float* home_grad, float* rep_grad, int64_t G_el,
+                                 int accumulate, hipStream_t stream);
+
+/* The root-mean-square norm in front of the experts, with the residual's addition, over T
+ * rows (any T, also 0, when nothing is written):
+ *   h = bf16_rne(x + res);  rstd = 1 / sqrt(mean(h^2) + eps);  out = bf16_rne(h * rstd * gamma)
+ * The norm is that of h as it is stored; squares are summed in fp32.
+ *   x, res  device bf16 [T, H]; res may be NULL (then h = x)
+ *   gamma   device bf16 [H]
+ *   out     device bf16 [T, H]
+ *   h       device bf16 [T, H] or NULL: the residual stream after this addition; may be x or
+ *           res itself (out may not)
+ *   rstd    device fp32 [T] or NULL: for the backward pass
+ * H % 8 == 0, H <= MOONEP_MAX_NORM, eps >= 0; pointers 16-byte aligned (rstd 4). */
+int moonep_rmsnorm(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                   int64_t T, int H, uint16_t* out, uint16_t* h, float* rstd, hipStream_t stream);
+
+/* Bytes of a row of H elements in 8 bits: H codes (OCP e4m3), H/32 scales (e8m0: byte b is
+ * 2^(b-127)), one for each 32 elements, and zeros up to a multiple of 16.  Host only.
+ * EINVAL unless H % 32 == 0; ELIMIT beyond MOONEP_MAX_NORM. */
+int64_t moonep_q8_row_bytes(int H);
+
+/* moonep_rmsnorm with its output in 8 bits: rows [T, moonep_q8_row_bytes(H)].  A block's
+ * scale is the smallest power of two that brings its largest magnitude to 448 or less, so
+ * nothing saturates; an element is rounded once, to nearest even, from fp32.  NaN and
+ * infinities become the code NaN in their place.  moonep_dispatch moves such rows as they
+ * are: pass them as bf16 rows of moonep_q8_row_bytes(H) / 2 elements; about half of
+ * the bytes of bf16 rows.  moonep_q8_unpack expands them on the other side. */
+int moonep_rmsnorm_q8(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
+                      int64_t T, int H, uint8_t* rows, uint16_t* h, float* rstd, hipStream_t stream);
+
+/* Expands N rows in 8 bits (moonep_rmsnorm_q8's, dispatched or not) to bf16 [N, H]:
+ * out = code * scale, exact wherever that is a normal bf16 number.  The bytes are taken as
+ * they are, so every row may be expanded, mapped or not. */
+int moonep_q8_unpack(const uint8_t* rows, int64_t N, int H, uint16_t* out, hipStream_t stream);
+
+/* Bytes of moonep_rmsnorm_bwd's workspace.  Host only.  Errors as in moonep_rmsnorm. */
+int64_t moonep_rmsnorm_bwd_workspace(int64_t T, int H);
+
+/* Backward of the norm, from the h and rstd that the forward call stored:
+ *   xhat = h * rstd,  gg = g_out * gamma
+ *   g_x = bf16_rne(rstd * (gg - xhat * mean(gg * xhat)) + g_h)    (the gradient of x and of res)
+ *   g_gamma = sum over rows of g_out * xhat                       (fp32)
+ *   g_out, h   device bf16 [T, H]      gamma  device bf16 [H]     rstd  device fp32 [T]
+ *   g_h        device bf16 [T, H] or NULL: the gradient that reaches h past the norm
+ *   workspace  device scratch of moonep_rmsnorm_bwd_workspace(T, H) bytes, 256-byte aligned;
+ *              calls whose kernels overlap in time must not share one
+ *   g_x        device bf16 [T, H], may be g_out, h or g_h itself
+ *   g_gamma    device fp32 [H], overwritten (zeros when T is 0)
+ * H % 8 == 0, H <= MOONEP_MAX_NORM; pointers 16-byte aligned (rstd 4).  Deterministic. */
+int moonep_rmsnorm_bwd(const uint16_t* g_out, const uint16_t* h, const uint16_t* gamma,
+                       const float* rstd, const uint16_t* g_h, int64_t T, int H, void* workspace,
+                       uint16_t* g_x, float* g_gamma, hipStream_t stream);
 
 /* Waits for `stream`, then copies the plan's statistics to the host.  The only call
  * that synchronises: the hot path itself never reads the plan back ("MoonshotAI/MoonEP
