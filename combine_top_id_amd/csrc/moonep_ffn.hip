@@ -21,14 +21,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define LDS __attribute__((address_space(3)))
 
-constexpr int kWaitVmcnt0 = 0x0F70;        // s_waitcnt vmcnt(0), other counters at maximum
-constexpr int kBK = 64;                    // k elements of a step
+constexpr int kBK = 32;                    // k elements of a step: one matrix instruction deep
+constexpr int kRing = 4;                   // steps in LDS: one being read, three in flight
 constexpr int kMaxSegs = 2 * MOONEP_MAX_E + MOONEP_MAX_R;
 constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: reads as zero
 constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
@@ -90,12 +91,25 @@ __device__ __forceinline__ int piece_count(const int32_t* plan, const moonep_siz
   return min(max(plan[s.o_hdr + H_NPIECES], 0), s.P_max);
 }
 
+// 16 bytes a lane from the buffer straight into LDS, to `to` + lane * 16.  In assembly: for
+// the builtin the compiler waits for every such load before any LDS read that it cannot
+// tell apart from it, which here is each one, and the next step's loads would never be in
+// flight during this step's products.  No register is written, so there is none to wait
+// for; arrive() is the wait.  (m0 holds the LDS address; gfx9 wants one instruction
+// between writing it and the load.)
+__device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, char* to) {
+  const uint32_t lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // operand tiles in LDS
 // ---------------------------------------------------------------------------------------
 // A step's tile holds kBK k of R rows (of P or Q).  Two forms:
-//   KC  memory is contiguous along k: LDS rows of 64 k (128 bytes), the 16-byte chunk c of
-//       row r at chunk c ^ (r & 7), so that the 16 rows of a fragment read hit all banks;
+//   KC  memory is contiguous along k: LDS rows of 32 k (64 bytes), the 16-byte chunk c of
+//       row r at chunk c ^ (r >> 2 & 3): a fragment's 16 rows x 4 chunks then lie in
+//       different banks for any 16 lanes that read at once;
 //   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, the
 //       32-byte unit u of row k at u ^ (k & 3 | (k >> 3 & 1) << 2), read transposed.
 // Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
@@ -113,8 +127,8 @@ struct Operand {
   __device__ __forceinline__ void init_kc(int wave, int lane, F rowoff) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int r = (i * NW + wave) * 8 + (lane >> 3);
-      voff[i] = rowoff(r) + (((lane & 7) ^ (lane >> 3)) << 4);
+      const int r = (i * NW + wave) * 16 + (lane >> 2);
+      voff[i] = rowoff(r) + (((lane & 3) ^ (lane >> 4)) << 4);
     }
   }
   // KS: rows of ld_bytes; columns at or past ncols read as zero
@@ -128,32 +142,30 @@ struct Operand {
       voff[i] = c * 8 < ncols ? k * ld_bytes + c * 16 : kOob;
     }
   }
-  // one step: `base` points at the step's first k, `kleft` k remain
-  __device__ __forceinline__ void issue(const char* base, int kleft, uint32_t ld_bytes, int lds,
-                                        char* smem, int wave, int lane) const {
-    const int64_t left = KS ? (int64_t)kleft * ld_bytes - lds : 0x7fffffff;
+  // One step into `to`: `base` points at the step's first k, `kleft` k remain (none, or
+  // less than none, past the end: the tile is filled with zeros).
+  __device__ __forceinline__ void issue(const char* base, int kleft, uint32_t ld_bytes, int skip,
+                                        char* to, int wave, int lane) const {
+    const int64_t left = KS ? max((int64_t)kleft * ld_bytes - skip, (int64_t)0) : 0x7fffffff;
     const int range = (int)(left < 0x7fffffff ? left : 0x7fffffff);
-    __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base), 0, range, kBufferFlags);
-    const uint32_t tail = !KS && ((((lane & 7) ^ (lane >> 3)) << 3) >= kleft) ? kOob : 0;
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const i32x4 rs{(int)at, (int)(at >> 32) & 0xFFFF, range, kBufferFlags};
+    const uint32_t tail = !KS && ((((lane & 3) ^ (lane >> 4)) << 3) >= kleft) ? kOob : 0;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS void*)(smem + (i * NW + wave) * 1024), 16,
-                                               voff[i] | tail, 0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) load_lds(rs, voff[i] | tail, to + (i * NW + wave) * 1024);
   }
 };
 
-// Fragment f (16 rows from row0 on, 32 k from kk*32) of a tile.
+// Fragment f (16 rows from row0 on) of a tile.
 template <int R, bool KS>
-__device__ __forceinline__ bf16x8 fragment(const char* tile, int row0, int f, int kk, int lane) {
+__device__ __forceinline__ bf16x8 fragment(const char* tile, int row0, int f, int lane) {
   if constexpr (!KS) {
-    const int a = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-    return *reinterpret_cast<const bf16x8*>(tile + (row0 + f * 16) * 128 + (a ^ (kk << 6)));
+    const int a = (lane & 15) * 64 + (((lane >> 4) ^ (lane >> 2 & 3)) << 4);
+    return *reinterpret_cast<const bf16x8*>(tile + row0 * 64 + a + f * 1024);
   } else {
     const int g = lane >> 4, j = (lane & 15) >> 2;
-    const int k = kk * 32 + g * 8 + j;
     const int sw = j | ((g & 1) << 2);
-    const int a = k * (R * 2) + (((row0 / 16 + f) ^ sw) << 5) + (lane & 3) * 8;
+    const int a = (g * 8 + j) * (R * 2) + (((row0 / 16 + f) ^ sw) << 5) + (lane & 3) * 8;
     union { s16x4 h[2]; bf16x8 v; } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a));
     u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a + 4 * R * 2));
@@ -175,30 +187,79 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[PF][QF]) {
     for (int q = 0; q < QF; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-template <int BP, int BQ, bool KSP, bool KSQ, int PF, int QF>
-__device__ __forceinline__ void step(const char* tp, const char* tq, int p0, int q0, int lane,
-                                     f32x4 (&acc)[PF][QF]) {
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    bf16x8 a[PF], b[QF];
-#pragma unroll
-    for (int p = 0; p < PF; ++p) a[p] = fragment<BP, KSP>(tp, p0, p, kk, lane);
-#pragma unroll
-    for (int q = 0; q < QF; ++q) b[q] = fragment<BQ, KSQ>(tq, q0, q, kk, lane);
-#pragma unroll
-    for (int p = 0; p < PF; ++p)
-#pragma unroll
-      for (int q = 0; q < QF; ++q)
-        acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p], b[q], acc[p][q], 0, 0, 0);
-  }
+// The tile of workgroup b in round `round` of a grid that is a multiple of 8: workgroups go
+// to the 8 XCDs in turn, so each XCD takes a run of consecutive tiles, which share rows and
+// weights in its L2.
+__device__ __forceinline__ int tile_of(int round, int b, int grid) {
+  return round * grid + (b & 7) * (grid >> 3) + (b >> 3);
 }
 
-// All of this wave's loads have arrived in LDS, then every wave's.
+// Tile `local` of an n x m grid of tiles: bands of kBand m, n by n within a band, so that 32
+// consecutive tiles are about as many m as n.
+constexpr int kBand = 4;
+__device__ __forceinline__ void band(int local, int m, int n, int* tm, int* tn) {
+  const int b = local / (kBand * n), r = local - b * kBand * n;
+  const int cnt = min(kBand, m - b * kBand);
+  *tm = b * kBand + r % cnt;
+  *tn = r / cnt;
+}
+
+// s_waitcnt with the given vmcnt, and with lgkmcnt(0)
+constexpr int wait_vm_lds(int vm) { return (vm & 15) | (vm >> 4) << 14 | 0x70; }
+
+// Waits until at most VM of this wave's loads are on their way and its LDS reads are done,
+// then for every wave of the workgroup.
+template <int VM>
 __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lds(VM));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// The products of a tile: `nk` steps; issue(i, to) starts the loads of step i (zeros past
+// the end).  While step i is multiplied out of registers, step i + 1 is read from LDS
+// into others, i + 2 and i + 3 are on their way and i + 4's loads go out into the buffer
+// that step i was read from.
+template <int BP, int BQ, bool KSP, bool KSQ, int NW, int PF, int QF, class Issue>
+__device__ __forceinline__ void products(char* smem, int nk, int p0, int q0, int lane,
+                                         f32x4 (&acc)[PF][QF], Issue issue) {
+  constexpr int kP = Operand<BP, KSP, NW>::kBytes, kStep = kP + Operand<BQ, KSQ, NW>::kBytes;
+  constexpr int kL = Operand<BP, KSP, NW>::kLoads + Operand<BQ, KSQ, NW>::kLoads;
+  static_assert(kRing == 4 && 3 * kL < 64);
+  bf16x8 a[2][PF], b[2][QF];
+  arrive<0>();                    // whatever an earlier tile still had in flight has landed
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) issue(i, smem + i * kStep);
+  arrive<3 * kL>();
+#pragma unroll
+  for (int p = 0; p < PF; ++p) a[0][p] = fragment<BP, KSP>(smem, p0, p, lane);
+#pragma unroll
+  for (int q = 0; q < QF; ++q) b[0][q] = fragment<BQ, KSQ>(smem + kP, q0, q, lane);
+  for (int i = 0; i < nk; i += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      arrive<2 * kL>();
+      issue(i + h + kRing, smem + ((i + h) & 3) * kStep);
+      const char* t = smem + ((i + h + 1) & 3) * kStep;
+#pragma unroll
+      for (int p = 0; p < PF; ++p) a[h ^ 1][p] = fragment<BP, KSP>(t, p0, p, lane);
+#pragma unroll
+      for (int q = 0; q < QF; ++q) b[h ^ 1][q] = fragment<BQ, KSQ>(t + kP, q0, q, lane);
+#pragma unroll
+      for (int q = 0; q < QF; ++q)
+#pragma unroll
+        for (int p = 0; p < PF; ++p)
+          acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
+      constexpr int kReads = PF * (KSP ? 2 : 1) + QF * (KSQ ? 2 : 1);
+      constexpr int kPer = PF * QF * 3 / 4 / kReads;
+#pragma unroll
+      for (int r = 0; r < kReads; ++r) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kPer > 0 ? kPer : 1, 0);
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
@@ -232,14 +293,14 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
 // ---------------------------------------------------------------------------------------
 
 template <int OP, int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ) void rows_kernel(const FfnArgs a) {
+__global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
   constexpr int NW = WP * WQ, PF = BP / WP / 16, QF = BQ / WQ / 16;
   constexpr bool KSP = OP == BWD1 || OP == BWD2;
   constexpr bool PAIR = OP == FWD1;            // P's rows are gate and up rows in turn
   using OpP = Operand<BP, KSP, NW>;
   using OpQ = Operand<BQ, false, NW>;
-  __shared__ __align__(1024) char smem[2][OpP::kBytes + OpQ::kBytes];
+  __shared__ __align__(1024) char smem[kRing * (OpP::kBytes + OpQ::kBytes)];
   __shared__ int pre[kMaxSegs];
   __shared__ int wsum[NW];
 
@@ -287,7 +348,9 @@ __global__ __launch_bounds__(64 * WP * WQ) void rows_kernel(const FfnArgs a) {
   const int tiles = mt_all * nt;
   const int nk = (K + kBK - 1) / kBK;
 
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  for (int round = 0; round * (int)gridDim.x < tiles; ++round) {
+    const int t = tile_of(round, blockIdx.x, gridDim.x);
+    if (t >= tiles) continue;
     // the segment of tile t: the first whose sum of tiles exceeds t / nt
     int sl = 0, sh = nseg - 1;
     const int want = t / nt;
@@ -300,8 +363,9 @@ __global__ __launch_bounds__(64 * WP * WQ) void rows_kernel(const FfnArgs a) {
     const int row0 = uni(g0.row0), n = uni(g0.n), w = uni(g0.w);
     const int mt = (n + BQ - 1) / BQ;
     const int local = t - (uni(pre[sl]) - mt) * nt;
-    const int tm = local % mt, tn = local / mt;
-    if (local < 0 || tn >= nt) continue;
+    if (local < 0 || local >= mt * nt) continue;
+    int tm, tn;
+    band(local, mt, nt, &tm, &tn);
     const int q0 = tm * BQ, nq = n - q0;                        // rows of this tile
     const uint16_t* W = w < a.s.E ? a.home_w + w * a.W_el : a.slot_w + (w - a.s.E) * a.W_el;
     if (OP == FWD2 || OP == BWD1) W += 2ll * a.I * a.H;
@@ -333,20 +397,11 @@ __global__ __launch_bounds__(64 * WP * WQ) void rows_kernel(const FfnArgs a) {
 
     f32x4 acc[PF][QF];
     clear(acc);
-    auto load = [&](int kt, char* to) {
-      P.issue(pb + (KSP ? (int64_t)kt * kBK * ldp : (int64_t)kt * kBK * 2), K - kt * kBK, ldp, n0 * 2,
-              to, wave, lane);
-      Q.issue(qb + (int64_t)kt * kBK * 2, K - kt * kBK, ldq, 0, to + OpP::kBytes, wave, lane);
-    };
-    load(0, smem[0]);
-    for (int kt = 0; kt < nk; ++kt) {
-      arrive();
-      char* cur = smem[kt & 1];
-      if (kt + 1 < nk) load(kt + 1, smem[(kt + 1) & 1]);
-      step<BP, BQ, KSP, false>(cur, cur + OpP::kBytes, wp * PF * 16, wq * QF * 16, lane, acc);
-    }
-    // the next tile's first loads overwrite the buffer that others may still read
-    __syncthreads();
+    products<BP, BQ, KSP, false, NW>(smem, nk, wp * PF * 16, wq * QF * 16, lane, acc, [&](int i, char* to) {
+      P.issue(pb + (KSP ? (int64_t)i * kBK * ldp : (int64_t)i * kBK * 2), K - i * kBK, ldp, n0 * 2, to,
+              wave, lane);
+      Q.issue(qb + (int64_t)i * kBK * 2, K - i * kBK, ldq, 0, to + OpP::kBytes, wave, lane);
+    });
 
     const int g = lane >> 4;
 #pragma unroll
@@ -434,12 +489,12 @@ struct GradArgs {
 };
 
 template <int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ) void grad_kernel(const GradArgs a) {
+__global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int NW = WP * WQ, PF = BP / WP / 16, QF = BQ / WQ / 16;
   using OpP = Operand<BP, true, NW>;
   using OpQ = Operand<BQ, true, NW>;
-  __shared__ __align__(1024) char smem[2][OpP::kBytes + OpQ::kBytes];
+  __shared__ __align__(1024) char smem[kRing * (OpP::kBytes + OpQ::kBytes)];
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int wp = wave % WP, wq = wave / WP;
   const int32_t* plan = a.plan;
@@ -449,11 +504,13 @@ __global__ __launch_bounds__(64 * WP * WQ) void grad_kernel(const GradArgs a) {
   const int p1 = (a.H + BP - 1) / BP, q1 = (2 * a.I + BQ - 1) / BQ;      // gate and up
   const int p2 = (a.I + BP - 1) / BP, q2 = (a.H + BQ - 1) / BQ;          // down
   const int per = p1 * q1 + p2 * q2;
-  const int64_t tiles = (int64_t)(s.E + np) * per;
+  const int tiles = (s.E + np) * per;
 
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int target = uni((int)(t / per));
-    int local = uni((int)(t - (int64_t)target * per));
+  for (int round = 0; round * (int)gridDim.x < tiles; ++round) {
+    const int t = tile_of(round, blockIdx.x, gridDim.x);
+    if (t >= tiles) continue;
+    const int target = t / per;
+    int local = t - target * per;
     Seg seg = load_seg(plan, s, target, np);
     int q = 0, qend = 0;                              // the fallback pieces of a home expert
     float* out;
@@ -470,8 +527,9 @@ __global__ __launch_bounds__(64 * WP * WQ) void grad_kernel(const GradArgs a) {
     }
     const bool down = local >= p1 * q1;
     if (down) local -= p1 * q1;
-    const int pt = down ? p2 : p1;
-    const int p0 = local % pt * BP, q0 = local / pt * BQ;
+    int tq, tp;
+    band(local, down ? q2 : q1, down ? p2 : p1, &tq, &tp);
+    const int p0 = tp * BP, q0 = tq * BQ;
     const int np_cols = down ? a.I : a.H, nq_cols = down ? a.H : 2 * a.I;
     const char* psrc = reinterpret_cast<const char*>(down ? a.h : a.recv);
     const char* qsrc = reinterpret_cast<const char*>(down ? a.g_y : a.g_gu);
@@ -483,41 +541,36 @@ __global__ __launch_bounds__(64 * WP * WQ) void grad_kernel(const GradArgs a) {
     P.init_ks(wave, lane, ldp, np_cols - p0);
     Q.init_ks(wave, lane, ldq, nq_cols - q0);
 
-    int row = uni(seg.row0), left = uni(seg.n);
     q = uni(q);
     qend = uni(qend);
-    // moves on to the next segment with rows; false when there is none
-    auto more = [&]() -> bool {
-      while (left <= 0 && q < qend) {
-        const Seg f = load_seg(plan, s, s.E + q, np);
-        ++q;
-        if (uni(f.w) == target && uni(f.n) > 0) {
-          row = uni(f.row0);
-          left = uni(f.n);
-        }
-      }
-      return left > 0;
-    };
-    auto load = [&](char* to) {
-      P.issue(psrc + (int64_t)row * ldp + p0 * 2, left, ldp, p0 * 2, to, wave, lane);
-      Q.issue(qsrc + (int64_t)row * ldq + q0 * 2, left, ldq, q0 * 2, to + OpP::kBytes, wave, lane);
-      row += kBK;
-      left -= kBK;
-    };
+    // the steps of the home group and of the fallback pieces
+    int row = uni(seg.row0), left = uni(seg.n), steps = (left + kBK - 1) / kBK;
+    for (int f = q; f < qend; ++f) {
+      const Seg fb = load_seg(plan, s, s.E + f, np);
+      if (uni(fb.w) == target) steps += (uni(fb.n) + kBK - 1) / kBK;
+    }
+    if (steps == 0 && a.accumulate) continue;
     f32x4 acc[PF][QF];
     clear(acc);
-    bool go = more();
-    if (!go && a.accumulate) continue;
-    if (go) load(smem[0]);
-    int cur = 0;
-    while (go) {
-      arrive();
-      go = more();
-      if (go) load(smem[cur ^ 1]);
-      step<BP, BQ, true, true>(smem[cur], smem[cur] + OpP::kBytes, wp * PF * 16, wq * QF * 16, lane, acc);
-      cur ^= 1;
-    }
-    __syncthreads();
+    if (steps)
+      products<BP, BQ, true, true, NW>(smem, steps, wp * PF * 16, wq * QF * 16, lane, acc, [&](int, char* to) {
+        while (left <= 0 && q < qend) {          // on to the next piece with rows
+          const Seg fb = load_seg(plan, s, s.E + q, np);
+          ++q;
+          if (uni(fb.w) == target && uni(fb.n) > 0) {
+            row = uni(fb.row0);
+            left = uni(fb.n);
+          }
+          // here, and not at some later use on the common path, where it would drain the ring
+          __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
+        }
+        P.issue(psrc + (int64_t)row * ldp + p0 * 2, left, ldp, p0 * 2, to, wave, lane);
+        Q.issue(qsrc + (int64_t)row * ldq + q0 * 2, left, ldq, q0 * 2, to + OpP::kBytes, wave, lane);
+        if (left > 0) {
+          row += kBK;
+          left -= kBK;
+        }
+      });
 
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
@@ -537,15 +590,15 @@ __global__ __launch_bounds__(64 * WP * WQ) void grad_kernel(const GradArgs a) {
 
 template <int OP>
 hipError_t launch_rows(FfnArgs a, hipStream_t st) {
-  constexpr int BP = 128, BQ = 128;
+  constexpr int BP = 256, BQ = 256;
   const int64_t segs = std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
   const int64_t mt = a.s.A / BQ + segs;
   const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
   constexpr int BN = OP == FWD1 ? BP / 2 : BP;
   const int64_t tiles = mt * ((N + BN - 1) / BN);
   a.tiles_bound = (int)mt;
-  const int grid = (int)std::min<int64_t>(tiles, 2 * kCus);
-  hipLaunchKernelGGL((rows_kernel<OP, BP, BQ, 2, 2>), dim3(grid), dim3(256), 0, st, a);
+  const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, kCus);
+  hipLaunchKernelGGL((rows_kernel<OP, BP, BQ, 4, 2>), dim3(grid), dim3(512), 0, st, a);
   return hipGetLastError();
 }
 
@@ -637,7 +690,7 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
   a.recv = recv; a.g_y = g_y; a.h = h; a.g_gu = g_gu;
   a.home = home_grad; a.rep = rep_grad; a.G_el = G_el;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((grad_kernel<128, 128, 2, 2>), dim3(2 * kCus), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((grad_kernel<256, 256, 4, 2>), dim3(kCus), dim3(512), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
