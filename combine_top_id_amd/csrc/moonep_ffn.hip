@@ -10,7 +10,7 @@
 // Every product is D[p, q] = sum_k P[p, k] * Q[q, k] with v_mfma_f32_16x16x32_bf16: P, the
 // side whose index runs along the output's rows in memory, is the instruction's first
 // operand, so a lane's four results are consecutive there.
-#include <cstring>
+#include <type_traits>
 
 #include "moonep_internal.h"
 
@@ -28,8 +28,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define LDS __attribute__((address_space(3)))
 
-constexpr int kBK = 32;                    // k elements of a step: one matrix instruction deep
-constexpr int kRing = 4;                   // steps in LDS: one being read, three in flight
+constexpr int kBK = 64;                    // k elements of a step: 128 bytes, a cache line
 constexpr int kMaxSegs = 2 * MOONEP_MAX_E + MOONEP_MAX_R;
 constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: reads as zero
 constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
@@ -91,25 +90,24 @@ __device__ __forceinline__ int piece_count(const int32_t* plan, const moonep_siz
   return min(max(plan[s.o_hdr + H_NPIECES], 0), s.P_max);
 }
 
-// 16 bytes a lane from the buffer straight into LDS, to `to` + lane * 16.  In assembly: for
-// the builtin the compiler waits for every such load before any LDS read that it cannot
-// tell apart from it, which here is each one, and the next step's loads would never be in
+// 16 bytes a lane from the buffer straight into LDS, to `to` + OFF + lane * 16.  In assembly:
+// for the builtin the compiler waits for every such load before any LDS read that it cannot
+// tell apart from it, which here is each one, and the next steps' loads would never be in
 // flight during this step's products.  No register is written, so there is none to wait
 // for; arrive() is the wait.  (m0 holds the LDS address; gfx9 wants one instruction
 // between writing it and the load.)
-__device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, char* to) {
-  const uint32_t lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)to);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
+template <int OFF>
+__device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(to), "v"(voff), "s"(rsrc), "i"(OFF) : "memory", "scc");
 }
 
 // ---------------------------------------------------------------------------------------
 // operand tiles in LDS
 // ---------------------------------------------------------------------------------------
 // A step's tile holds kBK k of R rows (of P or Q).  Two forms:
-//   KC  memory is contiguous along k: LDS rows of 32 k (64 bytes), the 16-byte chunk c of
-//       row r at chunk c ^ (r >> 2 & 3): a fragment's 16 rows x 4 chunks then lie in
-//       different banks for any 16 lanes that read at once;
+//   KC  memory is contiguous along k: LDS rows of 64 k (128 bytes), the 16-byte chunk c of
+//       row r at chunk c ^ (r & 7): the 16 lanes that read at once hit different banks;
 //   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, the
 //       32-byte unit u of row k at u ^ (k & 3 | (k >> 3 & 1) << 2), read transposed.
 // Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
@@ -121,51 +119,64 @@ struct Operand {
   static constexpr int kLoads = kBytes / 1024 / NW;
   static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes);
   uint32_t voff[kLoads];
+  int kc;                        // KC: this lane's first k inside a step
+  // the next step to load: its address and the k left from there (uniform)
+  const char* at;
+  int left;
+  uint32_t ld;                   // bytes of a row in memory
+  uint32_t skip;                 // KS: bytes of the row before `at`
+  i32x4 rs;
 
   // KC: rowoff(r) is the byte offset of LDS row r in memory, or kOob
   template <class F>
   __device__ __forceinline__ void init_kc(int wave, int lane, F rowoff) {
+    const int c = (lane & 7) ^ (lane >> 3);
+    kc = c * 8;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = (i * NW + wave) * 16 + (lane >> 2);
-      voff[i] = rowoff(r) + (((lane & 3) ^ (lane >> 4)) << 4);
-    }
+    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * 8 + (lane >> 3)) + c * 16;
   }
-  // KS: rows of ld_bytes; columns at or past ncols read as zero
-  __device__ __forceinline__ void init_ks(int wave, int lane, uint32_t ld_bytes, int ncols) {
+  // KS: columns at or past ncols read as zero
+  __device__ __forceinline__ void init_ks(int wave, int lane, int ncols) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int b = (i * NW + wave) * 1024 + lane * 16;
       const int k = b / (R * 2), cp = b % (R * 2) / 16;
       const int u = (cp >> 1) ^ ((k & 3) | ((k >> 3 & 1) << 2));
       const int c = u * 2 + (cp & 1);
-      voff[i] = c * 8 < ncols ? k * ld_bytes + c * 16 : kOob;
+      voff[i] = c * 8 < ncols ? k * ld + c * 16 : kOob;
     }
   }
-  // One step into `to`: `base` points at the step's first k, `kleft` k remain (none, or
-  // less than none, past the end: the tile is filled with zeros).
-  __device__ __forceinline__ void issue(const char* base, int kleft, uint32_t ld_bytes, int skip,
-                                        char* to, int wave, int lane) const {
-    const int64_t left = KS ? max((int64_t)kleft * ld_bytes - skip, (int64_t)0) : 0x7fffffff;
-    const int range = (int)(left < 0x7fffffff ? left : 0x7fffffff);
-    const uint64_t at = reinterpret_cast<uint64_t>(base);
-    const i32x4 rs{(int)at, (int)(at >> 32) & 0xFFFF, range, kBufferFlags};
-    const uint32_t tail = !KS && ((((lane & 3) ^ (lane >> 4)) << 3) >= kleft) ? kOob : 0;
+  // Makes the buffer descriptor of the next step and moves on.  Past the end everything is
+  // out of range, and the tile is filled with zeros.
+  __device__ __forceinline__ void next() {
+    const uint64_t p = reinterpret_cast<uint64_t>(at);
+    const int rows = max(min(left, kBK), 0);
+    const int range = !KS ? 0x7fffffff : rows ? rows * (int)ld - (int)skip : 0;
+    rs = i32x4{(int)p, (int)(p >> 32) & 0xFFFF, range, kBufferFlags};
+    if (!KS && left < kBK) {     // the last k, or none
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_lds(rs, voff[i] | tail, to + (i * NW + wave) * 1024);
+      for (int i = 0; i < kLoads; ++i) voff[i] |= kc >= left ? kOob : 0;
+    }
+    at += KS ? (uint64_t)ld * kBK : kBK * 2;
+    left -= kBK;
+  }
+  // load I of the step
+  template <int I, int OFF>
+  __device__ __forceinline__ void load(uint32_t to) const {
+    load_lds<I * NW * 1024 + OFF>(rs, voff[I], to);
   }
 };
 
-// Fragment f (16 rows from row0 on) of a tile.
+// Fragment f (16 rows from row0 on), k from kk * 32 on, of a tile.
 template <int R, bool KS>
-__device__ __forceinline__ bf16x8 fragment(const char* tile, int row0, int f, int lane) {
+__device__ __forceinline__ bf16x8 fragment(const char* tile, int row0, int f, int kk, int lane) {
   if constexpr (!KS) {
-    const int a = (lane & 15) * 64 + (((lane >> 4) ^ (lane >> 2 & 3)) << 4);
-    return *reinterpret_cast<const bf16x8*>(tile + row0 * 64 + a + f * 1024);
+    const int a = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    return *reinterpret_cast<const bf16x8*>(tile + row0 * 128 + (a ^ (kk << 6)) + f * 2048);
   } else {
     const int g = lane >> 4, j = (lane & 15) >> 2;
     const int sw = j | ((g & 1) << 2);
-    const int a = (g * 8 + j) * (R * 2) + (((row0 / 16 + f) ^ sw) << 5) + (lane & 3) * 8;
+    const int a = (g * 8 + j) * (R * 2) + (((row0 / 16 + f) ^ sw) << 5) + (lane & 3) * 8 + kk * 64 * R;
     union { s16x4 h[2]; bf16x8 v; } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a));
     u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a + 4 * R * 2));
@@ -217,48 +228,82 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
 }
 
-// The products of a tile: `nk` steps; issue(i, to) starts the loads of step i (zeros past
-// the end).  While step i is multiplied out of registers, step i + 1 is read from LDS
-// into others, i + 2 and i + 3 are on their way and i + 4's loads go out into the buffer
-// that step i was read from.
-template <int BP, int BQ, bool KSP, bool KSQ, int NW, int PF, int QF, class Issue>
-__device__ __forceinline__ void products(char* smem, int nk, int p0, int q0, int lane,
-                                         f32x4 (&acc)[PF][QF], Issue issue) {
-  constexpr int kP = Operand<BP, KSP, NW>::kBytes, kStep = kP + Operand<BQ, KSQ, NW>::kBytes;
-  constexpr int kL = Operand<BP, KSP, NW>::kLoads + Operand<BQ, KSQ, NW>::kLoads;
-  static_assert(kRing == 4 && 3 * kL < 64);
+template <int N, class F>
+__device__ __forceinline__ void times(F f) {
+  if constexpr (N > 0) {
+    times<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// The products of a tile, `nk` steps; before_next() runs before a step's loads are made.
+// Two steps' tiles are in LDS.  Each step is two matrix instructions deep: while its first
+// half is multiplied out of registers, the second is read from LDS into others; then
+// every wave has read the whole tile, and while the second half is multiplied, the first
+// half of the next step, whose loads went out a step ago, is read, and the step after
+// that starts to load over the tile just read.  One barrier a step.  Each half is cut into parts that
+// start a share of the loads, then spread a share of the LDS reads among their matrix
+// instructions.
+template <int BP, int BQ, bool KSP, bool KSQ, int NW, int PF, int QF, class F>
+__device__ __forceinline__ void products(char* smem, int nk, int wave, int p0, int q0, int lane,
+                                         f32x4 (&acc)[PF][QF], Operand<BP, KSP, NW>& P,
+                                         Operand<BQ, KSQ, NW>& Q, F before_next) {
+  using OpP = Operand<BP, KSP, NW>;
+  using OpQ = Operand<BQ, KSQ, NW>;
+  constexpr int kStep = OpP::kBytes + OpQ::kBytes, kL = OpP::kLoads + OpQ::kLoads;
+  constexpr int kParts = QF >= 4 ? 4 : QF, kM = PF * QF / kParts, kF = PF + QF;
+  static_assert(kL < 64 && QF % kParts == 0);
+  const uint32_t lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)smem + wave * 1024);
   bf16x8 a[2][PF], b[2][QF];
   arrive<0>();                    // whatever an earlier tile still had in flight has landed
+  times<2>([&](auto i) {
+    before_next();
+    P.next();
+    Q.next();
+    times<OpP::kLoads>([&](auto j) { P.template load<j, i * kStep>(lds); });
+    times<OpQ::kLoads>([&](auto j) { Q.template load<j, i * kStep + OpP::kBytes>(lds); });
+  });
+  arrive<kL>();
 #pragma unroll
-  for (int i = 0; i < kRing; ++i) issue(i, smem + i * kStep);
-  arrive<3 * kL>();
+  for (int p = 0; p < PF; ++p) a[0][p] = fragment<BP, KSP>(smem, p0, p, 0, lane);
 #pragma unroll
-  for (int p = 0; p < PF; ++p) a[0][p] = fragment<BP, KSP>(smem, p0, p, lane);
-#pragma unroll
-  for (int q = 0; q < QF; ++q) b[0][q] = fragment<BQ, KSQ>(smem + kP, q0, q, lane);
-  for (int i = 0; i < nk; i += 2) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      arrive<2 * kL>();
-      issue(i + h + kRing, smem + ((i + h) & 3) * kStep);
-      const char* t = smem + ((i + h + 1) & 3) * kStep;
-#pragma unroll
-      for (int p = 0; p < PF; ++p) a[h ^ 1][p] = fragment<BP, KSP>(t, p0, p, lane);
-#pragma unroll
-      for (int q = 0; q < QF; ++q) b[h ^ 1][q] = fragment<BQ, KSQ>(t + kP, q0, q, lane);
-#pragma unroll
-      for (int q = 0; q < QF; ++q)
-#pragma unroll
-        for (int p = 0; p < PF; ++p)
-          acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
-      constexpr int kReads = PF * (KSP ? 2 : 1) + QF * (KSQ ? 2 : 1);
-      constexpr int kPer = PF * QF * 3 / 4 / kReads;
-#pragma unroll
-      for (int r = 0; r < kReads; ++r) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, kPer > 0 ? kPer : 1, 0);
+  for (int q = 0; q < QF; ++q) b[0][q] = fragment<BQ, KSQ>(smem + OpP::kBytes, q0, q, 0, lane);
+  int cur = 0;
+  for (int i = 0; i < nk; ++i) {
+    times<2>([&](auto h) {
+      if constexpr (h == 1) {
+        before_next();
+        P.next();
+        Q.next();
+        arrive<0>();
       }
-    }
+      const uint32_t to = lds + cur;
+      const char* t = smem + (h ? cur ^ kStep : cur);
+      times<kParts>([&](auto c) {
+        times<kL>([&](auto j) {
+          if constexpr (h == 1 && j * kParts / kL == c) {
+            if constexpr (j < OpP::kLoads) P.template load<j, 0>(to);
+            else Q.template load<j - OpP::kLoads, OpP::kBytes>(to);
+          }
+        });
+        times<kF>([&](auto f) {
+          if constexpr (f * kParts / kF == c) {
+            if constexpr (f < PF) a[h ^ 1][f] = fragment<BP, KSP>(t, p0, f, h ^ 1, lane);
+            else b[h ^ 1][f - PF] = fragment<BQ, KSQ>(t + OpP::kBytes, q0, f - PF, h ^ 1, lane);
+          }
+        });
+        times<kM>([&](auto m) {
+          constexpr int p = m % PF, q = c * (QF / kParts) + m / PF;
+          acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
+        });
+        times<kM>([&](auto) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    cur ^= kStep;
   }
 }
 
@@ -300,7 +345,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) 
   constexpr bool PAIR = OP == FWD1;            // P's rows are gate and up rows in turn
   using OpP = Operand<BP, KSP, NW>;
   using OpQ = Operand<BQ, false, NW>;
-  __shared__ __align__(1024) char smem[kRing * (OpP::kBytes + OpQ::kBytes)];
+  __shared__ __align__(1024) char smem[2 * (OpP::kBytes + OpQ::kBytes)];
   __shared__ int pre[kMaxSegs];
   __shared__ int wsum[NW];
 
@@ -373,35 +418,33 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) 
 
     OpP P;
     OpQ Q;
-    const char* pb;
-    uint32_t ldp;
+    P.left = Q.left = K;
     if constexpr (!KSP) {
-      ldp = K * 2;
-      pb = reinterpret_cast<const char*>(W) + (int64_t)n0 * ldp;
+      P.ld = K * 2;
+      P.skip = 0;
+      P.at = reinterpret_cast<const char*>(W) + (int64_t)n0 * P.ld;
       P.init_kc(wave, lane, [&](int r) -> uint32_t {
         if (PAIR) {
           const int c = (r >> 6) * 32 + p_perm(r & 31);
-          return n0 + c < N ? (uint32_t)(c + (r >> 5 & 1) * a.I) * ldp : kOob;
+          return n0 + c < N ? (uint32_t)(c + (r >> 5 & 1) * a.I) * P.ld : kOob;
         }
         const int c = p_perm(r);
-        return n0 + c < N ? (uint32_t)c * ldp : kOob;
+        return n0 + c < N ? (uint32_t)c * P.ld : kOob;
       });
     } else {
-      ldp = N * 2;
-      pb = reinterpret_cast<const char*>(W) + n0 * 2;
-      P.init_ks(wave, lane, ldp, N - n0);
+      P.ld = N * 2;
+      P.skip = n0 * 2;
+      P.at = reinterpret_cast<const char*>(W) + P.skip;
+      P.init_ks(wave, lane, N - n0);
     }
-    const uint32_t ldq = K * 2;
-    const char* qb = reinterpret_cast<const char*>(a.in) + (int64_t)(row0 + q0) * ldq;
-    Q.init_kc(wave, lane, [&](int r) -> uint32_t { return r < nq ? r * ldq : kOob; });
+    Q.ld = K * 2;
+    Q.skip = 0;
+    Q.at = reinterpret_cast<const char*>(a.in) + (int64_t)(row0 + q0) * Q.ld;
+    Q.init_kc(wave, lane, [&](int r) -> uint32_t { return r < nq ? r * Q.ld : kOob; });
 
     f32x4 acc[PF][QF];
     clear(acc);
-    products<BP, BQ, KSP, false, NW>(smem, nk, wp * PF * 16, wq * QF * 16, lane, acc, [&](int i, char* to) {
-      P.issue(pb + (KSP ? (int64_t)i * kBK * ldp : (int64_t)i * kBK * 2), K - i * kBK, ldp, n0 * 2, to,
-              wave, lane);
-      Q.issue(qb + (int64_t)i * kBK * 2, K - i * kBK, ldq, 0, to + OpP::kBytes, wave, lane);
-    });
+    products<BP, BQ, KSP, false, NW>(smem, nk, wave, wp * PF * 16, wq * QF * 16, lane, acc, P, Q, [] {});
 
     const int g = lane >> 4;
 #pragma unroll
@@ -494,7 +537,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a)
   constexpr int NW = WP * WQ, PF = BP / WP / 16, QF = BQ / WQ / 16;
   using OpP = Operand<BP, true, NW>;
   using OpQ = Operand<BQ, true, NW>;
-  __shared__ __align__(1024) char smem[kRing * (OpP::kBytes + OpQ::kBytes)];
+  __shared__ __align__(1024) char smem[2 * (OpP::kBytes + OpQ::kBytes)];
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int wp = wave % WP, wq = wave / WP;
   const int32_t* plan = a.plan;
@@ -533,18 +576,26 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a)
     const int np_cols = down ? a.I : a.H, nq_cols = down ? a.H : 2 * a.I;
     const char* psrc = reinterpret_cast<const char*>(down ? a.h : a.recv);
     const char* qsrc = reinterpret_cast<const char*>(down ? a.g_y : a.g_gu);
-    const uint32_t ldp = np_cols * 2, ldq = nq_cols * 2;
     if (down) out += 2ll * a.I * a.H;
 
     OpP P;
     OpQ Q;
-    P.init_ks(wave, lane, ldp, np_cols - p0);
-    Q.init_ks(wave, lane, ldq, nq_cols - q0);
-
+    P.ld = np_cols * 2;
+    Q.ld = nq_cols * 2;
+    P.skip = p0 * 2;
+    Q.skip = q0 * 2;
+    P.init_ks(wave, lane, np_cols - p0);
+    Q.init_ks(wave, lane, nq_cols - q0);
+    auto start = [&](int row, int n) {
+      P.at = psrc + (int64_t)row * P.ld + P.skip;
+      Q.at = qsrc + (int64_t)row * Q.ld + Q.skip;
+      P.left = Q.left = n;
+    };
     q = uni(q);
     qend = uni(qend);
     // the steps of the home group and of the fallback pieces
-    int row = uni(seg.row0), left = uni(seg.n), steps = (left + kBK - 1) / kBK;
+    start(uni(seg.row0), uni(seg.n));
+    int steps = (P.left + kBK - 1) / kBK;
     for (int f = q; f < qend; ++f) {
       const Seg fb = load_seg(plan, s, s.E + f, np);
       if (uni(fb.w) == target) steps += (uni(fb.n) + kBK - 1) / kBK;
@@ -553,22 +604,13 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a)
     f32x4 acc[PF][QF];
     clear(acc);
     if (steps)
-      products<BP, BQ, true, true, NW>(smem, steps, wp * PF * 16, wq * QF * 16, lane, acc, [&](int, char* to) {
-        while (left <= 0 && q < qend) {          // on to the next piece with rows
+      products<BP, BQ, true, true, NW>(smem, steps, wave, wp * PF * 16, wq * QF * 16, lane, acc, P, Q, [&] {
+        while (P.left <= 0 && q < qend) {          // on to the next piece with rows
           const Seg fb = load_seg(plan, s, s.E + q, np);
           ++q;
-          if (uni(fb.w) == target && uni(fb.n) > 0) {
-            row = uni(fb.row0);
-            left = uni(fb.n);
-          }
+          if (uni(fb.w) == target && uni(fb.n) > 0) start(uni(fb.row0), uni(fb.n));
           // here, and not at some later use on the common path, where it would drain the ring
           __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
-        }
-        P.issue(psrc + (int64_t)row * ldp + p0 * 2, left, ldp, p0 * 2, to, wave, lane);
-        Q.issue(qsrc + (int64_t)row * ldq + q0 * 2, left, ldq, q0 * 2, to + OpP::kBytes, wave, lane);
-        if (left > 0) {
-          row += kBK;
-          left -= kBK;
         }
       });
 
