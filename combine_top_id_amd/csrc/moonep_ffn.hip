@@ -236,76 +236,118 @@ __device__ __forceinline__ void times(F f) {
   }
 }
 
-// The products of a tile, `nk` steps; before_next() runs before a step's loads are made.
-// Two steps' tiles are in LDS.  Each step is two matrix instructions deep: while its first
-// half is multiplied out of registers, the second is read from LDS into others; then
-// every wave has read the whole tile, and while the second half is multiplied, the first
-// half of the next step, whose loads went out a step ago, is read, and the step after
-// that starts to load over the tile just read.  One barrier a step.  Each half is cut into parts that
-// start a share of the loads, then spread a share of the LDS reads among their matrix
-// instructions.
-template <int BP, int BQ, bool KSP, bool KSQ, int NW, int PF, int QF, class F>
-__device__ __forceinline__ void products(char* smem, int nk, int wave, int p0, int q0, int lane,
-                                         f32x4 (&acc)[PF][QF], Operand<BP, KSP, NW>& P,
-                                         Operand<BQ, KSQ, NW>& Q, F before_next) {
-  using OpP = Operand<BP, KSP, NW>;
-  using OpQ = Operand<BQ, KSQ, NW>;
-  constexpr int kStep = OpP::kBytes + OpQ::kBytes, kL = OpP::kLoads + OpQ::kLoads;
-  constexpr int kParts = QF >= 4 ? 4 : QF, kM = PF * QF / kParts, kF = PF + QF;
-  static_assert(kL < 64 && QF % kParts == 0);
-  const uint32_t lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)smem + wave * 1024);
-  bf16x8 a[2][PF], b[2][QF];
-  arrive<0>();                    // whatever an earlier tile still had in flight has landed
-  times<2>([&](auto i) {
-    before_next();
-    P.next();
-    Q.next();
-    times<OpP::kLoads>([&](auto j) { P.template load<j, i * kStep>(lds); });
-    times<OpQ::kLoads>([&](auto j) { Q.template load<j, i * kStep + OpP::kBytes>(lds); });
-  });
-  arrive<kL>();
-#pragma unroll
-  for (int p = 0; p < PF; ++p) a[0][p] = fragment<BP, KSP>(smem, p0, p, 0, lane);
-#pragma unroll
-  for (int q = 0; q < QF; ++q) b[0][q] = fragment<BQ, KSQ>(smem + OpP::kBytes, q0, q, 0, lane);
-  int cur = 0;
-  for (int i = 0; i < nk; ++i) {
-    times<2>([&](auto h) {
-      if constexpr (h == 1) {
-        before_next();
-        P.next();
-        Q.next();
-        arrive<0>();
-      }
-      const uint32_t to = lds + cur;
-      const char* t = smem + (h ? cur ^ kStep : cur);
-      times<kParts>([&](auto c) {
-        times<kL>([&](auto j) {
-          if constexpr (h == 1 && j * kParts / kL == c) {
-            if constexpr (j < OpP::kLoads) P.template load<j, 0>(to);
-            else Q.template load<j - OpP::kLoads, OpP::kBytes>(to);
-          }
-        });
-        times<kF>([&](auto f) {
-          if constexpr (f * kParts / kF == c) {
-            if constexpr (f < PF) a[h ^ 1][f] = fragment<BP, KSP>(t, p0, f, h ^ 1, lane);
-            else b[h ^ 1][f - PF] = fragment<BQ, KSQ>(t + OpP::kBytes, q0, f - PF, h ^ 1, lane);
-          }
-        });
-        times<kM>([&](auto m) {
-          constexpr int p = m % PF, q = c * (QF / kParts) + m / PF;
-          acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
-        });
-        times<kM>([&](auto) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    });
-    cur ^= kStep;
+// A tile's geometry: BP x BQ results by WP x WQ waves; LDS holds the tiles of NB steps of P
+// and NB - 1 of Q.
+template <int BP_, int BQ_, int WP_, int WQ_, int NB_>
+struct Geometry {
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NB = NB_, NW = WP * WQ;
+  static constexpr int PF = BP / WP / 16, QF = BQ / WQ / 16;
+};
+
+// The products of one tile after another.  Each step is two matrix instructions deep: while
+// its first half is multiplied out of registers, the second is read from LDS into others;
+// then every wave has read the whole tile, and while the second half is multiplied, the
+// first half of the next step is read, and the tiles of Q's step NB - 1 and P's step NB
+// further on start to load over the ones just read.  One barrier a step.  Each half is
+// cut into parts that start a share of the loads, then spread a share of the LDS reads
+// among their matrix instructions.  begin() starts a tile's first loads: it is called before
+// the results of the tile before are written, which hides them.
+template <class G, bool KSP, bool KSQ>
+struct Pipe {
+  using OpP = Operand<G::BP, KSP, G::NW>;
+  using OpQ = Operand<G::BQ, KSQ, G::NW>;
+  static constexpr int PF = G::PF, QF = G::QF, NB = G::NB;
+  static constexpr int kP = OpP::kBytes, kQ = OpQ::kBytes, kLP = OpP::kLoads, kLQ = OpQ::kLoads;
+  static constexpr int kQ0 = NB * kP, kLds = NB * kP + (NB - 1) * kQ;
+  static constexpr int kParts = QF >= 4 ? 4 : QF, kM = PF * QF / kParts, kF = PF + QF;
+  static_assert(QF % kParts == 0 && (NB - 1) * kLP + (NB - 2) * kLQ < 64 && kLds <= 160 * 1024);
+  char* smem;
+  uint32_t lds;                   // this wave's first LDS byte of a load
+  int wave, lane, p0, q0;
+  OpP P;
+  OpQ Q;
+
+  __device__ __forceinline__ Pipe(char* smem_, int wave_, int lane_)
+      : smem(smem_), wave(wave_), lane(lane_), p0(wave_ % G::WP * PF * 16), q0(wave_ / G::WP * QF * 16) {
+    lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)smem + wave * 1024);
   }
-}
+
+  template <class FP, class FQ>
+  __device__ __forceinline__ void begin(FP before_p, FQ before_q) {
+    arrive<0>();                  // the tile before is read, and its loads past the end have landed
+    times<NB>([&](auto i) {
+      before_p();
+      P.next();
+      times<kLP>([&](auto j) { P.template load<j, i * kP>(lds); });
+      if constexpr (i < NB - 1) {
+        before_q();
+        Q.next();
+        times<kLQ>([&](auto j) { Q.template load<j, kQ0 + i * kQ>(lds); });
+      }
+    });
+  }
+
+  template <bool ALL, class FP, class FQ>
+  __device__ __forceinline__ void steps(int nk, int live, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
+    bf16x8 a[2][PF], b[2][QF];
+#pragma unroll
+    for (int p = 0; p < PF; ++p) a[0][p] = fragment<G::BP, KSP>(smem, p0, p, 0, lane);
+#pragma unroll
+    for (int q = 0; q < QF; ++q) b[0][q] = fragment<G::BQ, KSQ>(smem + kQ0, q0, q, 0, lane);
+    int cp = 0, cq = kQ0;         // this step's tiles
+    for (int i = 0; i < nk; ++i) {
+      const int np = cp == (NB - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NB - 2) * kQ ? kQ0 : cq + kQ;
+      times<2>([&](auto h) {
+        if constexpr (h == 1) {
+          before_q();
+          Q.next();
+          before_p();
+          P.next();
+          arrive<kLP + (NB - 3) * (kLP + kLQ)>();
+        }
+        const uint32_t top = lds + cp, toq = lds + cq;
+        const char* tp = smem + (h ? np : cp);
+        const char* tq = smem + (h ? nq : cq);
+        times<kParts>([&](auto c) {
+          times<kLP + kLQ>([&](auto j) {
+            if constexpr (h == 1 && j * kParts / (kLP + kLQ) == c) {
+              if constexpr (j < kLQ) Q.template load<j, 0>(toq);
+              else P.template load<j - kLQ, 0>(top);
+            }
+          });
+          times<kF>([&](auto f) {
+            if constexpr (f * kParts / kF == c) {
+              if constexpr (f < PF) a[h ^ 1][f] = fragment<G::BP, KSP>(tp, p0, f, h ^ 1, lane);
+              else b[h ^ 1][f - PF] = fragment<G::BQ, KSQ>(tq, q0, f - PF, h ^ 1, lane);
+            }
+          });
+          if (ALL || c * (QF / kParts) * 16 < live)
+            times<kM>([&](auto m) {
+              constexpr int p = m % PF, q = c * (QF / kParts) + m / PF;
+              acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
+            });
+          if constexpr (ALL)
+            times<kM>([&](auto) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+      cp = np;
+      cq = nq;
+    }
+  }
+
+  // `live`: how many of the wave's rows of Q are there.  Where they are not all, the matrix
+  // instructions of the rest are left out.
+  template <class FP, class FQ>
+  __device__ __forceinline__ void run(int nk, int live, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
+    arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
+    if (live >= QF * 16) steps<true>(nk, live, acc, before_p, before_q);
+    else steps<false>(nk, live, acc, before_p, before_q);
+  }
+};
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -337,87 +379,83 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
 // the row products: forward, and the rows' gradient
 // ---------------------------------------------------------------------------------------
 
-template <int OP, int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) {
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_sums(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+template <int OP, class G>
+__global__ __launch_bounds__(64 * G::NW, 1) void rows_kernel(const FfnArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
-  constexpr int NW = WP * WQ, PF = BP / WP / 16, QF = BQ / WQ / 16;
+  constexpr int BP = G::BP, BQ = G::BQ, WP = G::WP, PF = G::PF, QF = G::QF;
   constexpr bool KSP = OP == BWD1 || OP == BWD2;
   constexpr bool PAIR = OP == FWD1;            // P's rows are gate and up rows in turn
-  using OpP = Operand<BP, KSP, NW>;
-  using OpQ = Operand<BQ, false, NW>;
-  __shared__ __align__(1024) char smem[2 * (OpP::kBytes + OpQ::kBytes)];
-  __shared__ int pre[kMaxSegs];
-  __shared__ int wsum[NW];
+  constexpr int BN = PAIR ? BP / 2 : BP;       // output columns of a tile
+  using Tiles = Pipe<G, KSP, false>;
+  __shared__ __align__(1024) char smem[Tiles::kLds];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int wp = wave % WP, wq = wave / WP;
   const int32_t* plan = a.plan;
+  if (uni(plan[a.s.o_hdr + H_STATUS]) != 0) return;
   const int np = uni(piece_count(plan, a.s));
-  const bool valid = uni(plan[a.s.o_hdr + H_STATUS]) == 0;
-  const int nseg = valid ? a.s.E + np : 0;
-
-  // inclusive sums of the segments' row tiles
-  {
-    constexpr int PER = (kMaxSegs + 64 * NW - 1) / (64 * NW);
-    int cnt[PER], sum = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid * PER + j;
-      cnt[j] = 0;
-      if (i < nseg) cnt[j] = (load_seg(plan, a.s, i, np).n + BQ - 1) / BQ;
-      sum += cnt[j];
-    }
-    int inc = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_up(inc, d);
-      if (lane >= d) inc += o;
-    }
-    if (lane == 63) wsum[wave] = inc;
-    __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < wave; ++w) before += wsum[w];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid * PER + j;
-      before += cnt[j];
-      if (i < nseg) pre[i] = before;
-    }
-    __syncthreads();
-  }
+  const int nseg = a.s.E + np;
   const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
-  const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;          // output columns
-  constexpr int BN = PAIR ? BP / 2 : BP;
+  const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
   const int nt = (N + BN - 1) / BN;
-  const int mt_all = nseg ? min(uni(pre[nseg - 1]), a.tiles_bound) : 0;
-  const int tiles = mt_all * nt;
   const int nk = (K + kBK - 1) / kBK;
 
-  for (int round = 0; round * (int)gridDim.x < tiles; ++round) {
+  // Lane l sums the row tiles of segments [l * per, l * per + per); a tile is then found by
+  // comparing its number with all sums at once, in each wave on its own: no LDS, no
+  // barrier.
+  const int per = (nseg + 63) / 64;
+  int sum = 0;
+  for (int j = 0; j < per; ++j) {
+    const int i = lane * per + j;
+    if (i < nseg) sum += (load_seg(plan, a.s, i, np).n + BQ - 1) / BQ;
+  }
+  sum = wave_sums(sum, lane);
+  const int tiles = min(__builtin_amdgcn_readlane(sum, 63), a.tiles_bound) * nt;
+
+  Tiles pipe(smem, wave, lane);
+  int row0 = 0, nq = 0, n0 = 0;                 // of the tile that is set up
+  auto none = [] {};
+
+  // sets up the tile of round `round`; false where there is none
+  auto set_up = [&](int round) -> bool {
     const int t = tile_of(round, blockIdx.x, gridDim.x);
-    if (t >= tiles) continue;
-    // the segment of tile t: the first whose sum of tiles exceeds t / nt
-    int sl = 0, sh = nseg - 1;
+    if (t < 0 || t >= tiles) return false;
     const int want = t / nt;
-    while (sl < sh) {
-      const int mid = (sl + sh) / 2;
-      if (pre[mid] > want) sh = mid; else sl = mid + 1;
+    const int l = __builtin_popcountll(__ballot(sum <= want));
+    int below = l ? __builtin_amdgcn_readlane(sum, l - 1) : 0;
+    Seg g{0, 0, 0};
+    if (lane < per) g = load_seg(plan, a.s, l * per + lane, np);
+    const int cnt = (g.n + BQ - 1) / BQ;
+    int inc = cnt, j = 0;
+    if (per > 1) {
+      inc = wave_sums(cnt, lane);
+      j = __builtin_popcountll(__ballot(lane < per && below + inc <= want));
+      if (j >= per) return false;               // the plan changed under the call
+      below += j ? __builtin_amdgcn_readlane(inc, j - 1) : 0;
     }
-    sl = uni(sl);
-    const Seg g0 = load_seg(plan, a.s, sl, np);
-    const int row0 = uni(g0.row0), n = uni(g0.n), w = uni(g0.w);
-    const int mt = (n + BQ - 1) / BQ;
-    const int local = t - (uni(pre[sl]) - mt) * nt;
-    if (local < 0 || local >= mt * nt) continue;
+    const int seg_row = __builtin_amdgcn_readlane(g.row0, j), n = __builtin_amdgcn_readlane(g.n, j);
+    const int w = __builtin_amdgcn_readlane(g.w, j), mt = __builtin_amdgcn_readlane(cnt, j);
     int tm, tn;
-    band(local, mt, nt, &tm, &tn);
-    const int q0 = tm * BQ, nq = n - q0;                        // rows of this tile
+    if (mt <= 0) return false;
+    band(t - below * nt, mt, nt, &tm, &tn);
+    row0 = seg_row + tm * BQ;
+    nq = n - tm * BQ;
+    n0 = tn * BN;
+    if (nq <= 0 || n0 >= N) return false;
     const uint16_t* W = w < a.s.E ? a.home_w + w * a.W_el : a.slot_w + (w - a.s.E) * a.W_el;
     if (OP == FWD2 || OP == BWD1) W += 2ll * a.I * a.H;
-    const int n0 = tn * BN;
-
-    OpP P;
-    OpQ Q;
+    auto& P = pipe.P;
+    auto& Q = pipe.Q;
     P.left = Q.left = K;
     if constexpr (!KSP) {
       P.ld = K * 2;
@@ -439,23 +477,32 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) 
     }
     Q.ld = K * 2;
     Q.skip = 0;
-    Q.at = reinterpret_cast<const char*>(a.in) + (int64_t)(row0 + q0) * Q.ld;
+    Q.at = reinterpret_cast<const char*>(a.in) + (int64_t)row0 * Q.ld;
     Q.init_kc(wave, lane, [&](int r) -> uint32_t { return r < nq ? r * Q.ld : kOob; });
+    return true;
+  };
 
+  bool have = set_up(0);
+  if (have) pipe.begin(none, none);
+  for (int round = 1; have; ++round) {
     f32x4 acc[PF][QF];
     clear(acc);
-    products<BP, BQ, KSP, false, NW>(smem, nk, wave, wp * PF * 16, wq * QF * 16, lane, acc, P, Q, [] {});
+    const int trow = row0, tq = nq, tn0 = n0;
+    const bool idle = tn0 + (PAIR ? wp * PF * 8 : wp * PF * 16) >= N;     // no columns for this wave
+    pipe.run(nk, idle ? 0 : tq - wq * QF * 16, acc, none, none);
+    have = set_up(round);
+    if (have) pipe.begin(none, none);
 
     const int g = lane >> 4;
 #pragma unroll
     for (int q = 0; q < QF; ++q) {
       const int r = wq * QF * 16 + q * 16 + (lane & 15);
-      if (r >= nq) continue;
-      const int64_t row = row0 + q0 + r;
+      if (r >= tq) continue;
+      const int64_t row = trow + r;
       if constexpr (OP == FWD1) {
 #pragma unroll
         for (int pb4 = 0; pb4 < PF; pb4 += 4) {
-          const int c = n0 + (wp * PF + pb4) * 8 + g * 8;       // 64 P rows give 32 columns
+          const int c = tn0 + (wp * PF + pb4) * 8 + g * 8;       // 64 P rows give 32 columns
           if (c >= N) continue;
           u32x4 h, vg, vu;
 #pragma unroll
@@ -477,7 +524,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) 
       } else if constexpr (OP == FWD2) {
 #pragma unroll
         for (int p = 0; p < PF; p += 2) {
-          const int c = n0 + (wp * PF + p) * 16 + g * 8;
+          const int c = tn0 + (wp * PF + p) * 16 + g * 8;
           if (c >= N) continue;
           u32x4 v;
 #pragma unroll
@@ -488,7 +535,7 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void rows_kernel(const FfnArgs a) 
       } else {
 #pragma unroll
         for (int p = 0; p < PF; ++p) {
-          const int c = n0 + (wp * PF + p) * 16 + g * 4;
+          const int c = tn0 + (wp * PF + p) * 16 + g * 4;
           if (c >= N) continue;
           const f32x4 d = acc[p][q];
           if constexpr (OP == BWD2) {
@@ -531,14 +578,13 @@ struct GradArgs {
   int64_t G_el;
 };
 
-template <int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a) {
+template <class G>
+__global__ __launch_bounds__(64 * G::NW, 1) void grad_kernel(const GradArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
-  constexpr int NW = WP * WQ, PF = BP / WP / 16, QF = BQ / WQ / 16;
-  using OpP = Operand<BP, true, NW>;
-  using OpQ = Operand<BQ, true, NW>;
-  __shared__ __align__(1024) char smem[2 * (OpP::kBytes + OpQ::kBytes)];
-  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  constexpr int BP = G::BP, BQ = G::BQ, WP = G::WP, PF = G::PF, QF = G::QF;
+  using Tiles = Pipe<G, true, true>;
+  __shared__ __align__(1024) char smem[Tiles::kLds];
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int wp = wave % WP, wq = wave / WP;
   const int32_t* plan = a.plan;
   const moonep_sizes& s = a.s;
@@ -549,99 +595,138 @@ __global__ __launch_bounds__(64 * WP * WQ, 1) void grad_kernel(const GradArgs a)
   const int per = p1 * q1 + p2 * q2;
   const int tiles = (s.E + np) * per;
 
-  for (int round = 0; round * (int)gridDim.x < tiles; ++round) {
-    const int t = tile_of(round, blockIdx.x, gridDim.x);
-    if (t >= tiles) continue;
-    const int target = t / per;
-    int local = t - target * per;
-    Seg seg = load_seg(plan, s, target, np);
-    int q = 0, qend = 0;                              // the fallback pieces of a home expert
-    float* out;
-    if (target < s.E) {
-      if (!valid) seg.n = 0;
-      if (np) {
-        q = min(max(plan[s.o_pfirst + target], 0), np);
-        qend = q + min(max(plan[s.o_pnum + target], 0), np - q);
-      }
-      out = a.home + target * a.G_el;
-    } else {
-      if (seg.n == 0 || seg.w < s.E) continue;        // a fallback piece: in its home's sum
-      out = a.rep + (seg.w - s.E) * a.G_el;
-    }
-    const bool down = local >= p1 * q1;
-    if (down) local -= p1 * q1;
-    int tq, tp;
-    band(local, down ? q2 : q1, down ? p2 : p1, &tq, &tp);
-    const int p0 = tp * BP, q0 = tq * BQ;
-    const int np_cols = down ? a.I : a.H, nq_cols = down ? a.H : 2 * a.I;
-    const char* psrc = reinterpret_cast<const char*>(down ? a.h : a.recv);
-    const char* qsrc = reinterpret_cast<const char*>(down ? a.g_y : a.g_gu);
-    if (down) out += 2ll * a.I * a.H;
+  Tiles pipe(smem, wave, lane);
+  auto& P = pipe.P;
+  auto& Q = pipe.Q;
+  // of the tile that is set up
+  int round = 0, target = 0, p0 = 0, q0 = 0, pcols = 0, qcols = 0, steps = 0;
+  int fp = 0, fq = 0, fend = 0;                 // the fallback pieces that each side has yet to take
+  const char *psrc = nullptr, *qsrc = nullptr;
+  float* out = nullptr;
 
-    OpP P;
-    OpQ Q;
-    P.ld = np_cols * 2;
-    Q.ld = nq_cols * 2;
-    P.skip = p0 * 2;
-    Q.skip = q0 * 2;
-    P.init_ks(wave, lane, np_cols - p0);
-    Q.init_ks(wave, lane, nq_cols - q0);
-    auto start = [&](int row, int n) {
-      P.at = psrc + (int64_t)row * P.ld + P.skip;
-      Q.at = qsrc + (int64_t)row * Q.ld + Q.skip;
-      P.left = Q.left = n;
-    };
-    q = uni(q);
-    qend = uni(qend);
-    // the steps of the home group and of the fallback pieces
-    start(uni(seg.row0), uni(seg.n));
-    int steps = (P.left + kBK - 1) / kBK;
-    for (int f = q; f < qend; ++f) {
+  auto start = [](auto& side, const char* src, int row, int n) {
+    side.at = src + (int64_t)row * side.ld + side.skip;
+    side.left = n;
+  };
+  // on to the next piece with rows, where a side has done its segment
+  auto walk = [&](auto& side, const char* src, int& f) {
+    while (side.left <= 0 && f < fend) {
       const Seg fb = load_seg(plan, s, s.E + f, np);
-      if (uni(fb.w) == target) steps += (uni(fb.n) + kBK - 1) / kBK;
+      ++f;
+      if (uni(fb.w) == target && uni(fb.n) > 0) start(side, src, uni(fb.row0), uni(fb.n));
+      // here, and not at some later use on the common path, where it would drain the ring
+      __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
     }
-    if (steps == 0 && a.accumulate) continue;
+  };
+  auto walk_p = [&] { walk(P, psrc, fp); };
+  auto walk_q = [&] { walk(Q, qsrc, fq); };
+
+  // sets up the workgroup's next tile; false where there is none
+  auto set_up = [&]() -> bool {
+    for (;; ) {
+      const int first = tile_of(round, 0, gridDim.x);
+      const int t = tile_of(round, blockIdx.x, gridDim.x);
+      ++round;
+      if (first >= tiles) return false;
+      if (t >= tiles) continue;
+      target = t / per;
+      int local = t - target * per;
+      Seg seg = load_seg(plan, s, target, np);
+      fp = fq = fend = 0;
+      if (target < s.E) {
+        if (!valid) seg.n = 0;
+        if (np) {
+          fp = uni(min(max(plan[s.o_pfirst + target], 0), np));
+          fend = fp + uni(min(max(plan[s.o_pnum + target], 0), np - fp));
+        }
+        out = a.home + target * a.G_el;
+      } else {
+        const int w = uni(seg.w);
+        if (uni(seg.n) == 0 || w < s.E) continue;       // a fallback piece: in its home's sum
+        out = a.rep + (w - s.E) * a.G_el;
+      }
+      fq = fp;
+      const bool down = local >= p1 * q1;
+      if (down) local -= p1 * q1;
+      int tq, tp;
+      band(local, down ? q2 : q1, down ? p2 : p1, &tq, &tp);
+      p0 = tp * BP;
+      q0 = tq * BQ;
+      pcols = down ? a.I : a.H;
+      qcols = down ? a.H : 2 * a.I;
+      psrc = reinterpret_cast<const char*>(down ? a.h : a.recv);
+      qsrc = reinterpret_cast<const char*>(down ? a.g_y : a.g_gu);
+      if (down) out += 2ll * a.I * a.H;
+      P.ld = pcols * 2;
+      Q.ld = qcols * 2;
+      P.skip = p0 * 2;
+      Q.skip = q0 * 2;
+      P.init_ks(wave, lane, pcols - p0);
+      Q.init_ks(wave, lane, qcols - q0);
+      start(P, psrc, uni(seg.row0), uni(seg.n));
+      start(Q, qsrc, uni(seg.row0), uni(seg.n));
+      steps = (P.left + kBK - 1) / kBK;
+      for (int f = fp; f < fend; ++f) {
+        const Seg fb = load_seg(plan, s, s.E + f, np);
+        if (uni(fb.w) == target) steps += (uni(fb.n) + kBK - 1) / kBK;
+      }
+      if (steps == 0 && a.accumulate) continue;
+      return true;
+    }
+  };
+
+  bool have = set_up();
+  if (have && steps) pipe.begin(walk_p, walk_q);
+  while (have) {
     f32x4 acc[PF][QF];
     clear(acc);
-    if (steps)
-      products<BP, BQ, true, true, NW>(smem, steps, wave, wp * PF * 16, wq * QF * 16, lane, acc, P, Q, [&] {
-        while (P.left <= 0 && q < qend) {          // on to the next piece with rows
-          const Seg fb = load_seg(plan, s, s.E + q, np);
-          ++q;
-          if (uni(fb.w) == target && uni(fb.n) > 0) start(uni(fb.row0), uni(fb.n));
-          // here, and not at some later use on the common path, where it would drain the ring
-          __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
-        }
-      });
+    const int tp0 = p0, tq0 = q0, tpc = pcols, tqc = qcols;
+    const bool add = a.accumulate && target < s.E;
+    float* const tout = out;
+    const bool idle = tp0 + wp * PF * 16 >= tpc;
+    if (steps) pipe.run(steps, idle ? 0 : tqc - tq0 - wq * QF * 16, acc, walk_p, walk_q);
+    have = set_up();
+    if (have && steps) pipe.begin(walk_p, walk_q);
 
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
-      const int r = q0 + (wq * QF + f) * 16 + (lane & 15);
-      if (r >= nq_cols) continue;
+      const int r = tq0 + (wq * QF + f) * 16 + (lane & 15);
+      if (r >= tqc) continue;
 #pragma unroll
       for (int p = 0; p < PF; ++p) {
-        const int c = p0 + (wp * PF + p) * 16 + (lane >> 4) * 4;
-        if (c >= np_cols) continue;
-        f32x4* o = reinterpret_cast<f32x4*>(out + (int64_t)r * np_cols + c);
-        *o = a.accumulate && target < s.E ? *o + acc[p][f] : acc[p][f];
+        const int c = tp0 + (wp * PF + p) * 16 + (lane >> 4) * 4;
+        if (c >= tpc) continue;
+        f32x4* o = reinterpret_cast<f32x4*>(tout + (int64_t)r * tpc + c);
+        *o = add ? *o + acc[p][f] : acc[p][f];
       }
     }
   }
 #endif
 }
 
-template <int OP>
-hipError_t launch_rows(FfnArgs a, hipStream_t st) {
-  constexpr int BP = 256, BQ = 256;
+using Large = Geometry<256, 256, 4, 2, 3>;
+using Medium = Geometry<128, 64, 2, 2, 3>;
+using Small = Geometry<128, 32, 2, 2, 4>;
+
+template <int OP, class G>
+hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
   const int64_t segs = std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
-  const int64_t mt = a.s.A / BQ + segs;
+  const int64_t mt = a.s.A / G::BQ + segs;
   const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
-  constexpr int BN = OP == FWD1 ? BP / 2 : BP;
+  constexpr int BN = OP == FWD1 ? G::BP / 2 : G::BP;
   const int64_t tiles = mt * ((N + BN - 1) / BN);
   a.tiles_bound = (int)mt;
-  const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, kCus);
-  hipLaunchKernelGGL((rows_kernel<OP, BP, BQ, 4, 2>), dim3(grid), dim3(512), 0, st, a);
+  const int grid = (int)std::min<int64_t>((tiles + 7) / 8 * 8, per_cu * kCus);
+  hipLaunchKernelGGL((rows_kernel<OP, G>), dim3(grid), dim3(64 * G::NW), 0, st, a);
   return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
+  const int64_t mean = a.s.A / a.s.E;
+  if (mean <= 24) return launch_rows_as<OP, Small>(a, 2, st);
+  if (mean <= 96) return launch_rows_as<OP, Medium>(a, 2, st);
+  return launch_rows_as<OP, Large>(a, 1, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -732,7 +817,7 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
   a.recv = recv; a.g_y = g_y; a.h = h; a.g_gu = g_gu;
   a.home = home_grad; a.rep = rep_grad; a.G_el = G_el;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((grad_kernel<256, 256, 4, 2>), dim3(kCus), dim3(512), 0, stream, a);
+  hipLaunchKernelGGL((grad_kernel<Large>), dim3(kCus), dim3(512), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
