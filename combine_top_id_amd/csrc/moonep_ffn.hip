@@ -7,9 +7,12 @@
 //                  g_recv = g_gate Wg + g_up Wu
 //   weights'       g_Wg = g_gate^T x, g_Wu = g_up^T x, g_Wd = g_y^T h
 //
-// Every product is D[p, q] = sum_k P[p, k] * Q[q, k] with v_mfma_f32_16x16x32_bf16: P, the
-// side whose index runs along the output's rows in memory, is the instruction's first
-// operand, so a lane's four results are consecutive there.
+// Every product is D[q, p] = sum_k Q[q, k] * P[p, k] with v_mfma_f32_16x16x32_bf16, p being the
+// index along the output's rows in memory: a lane holds four q of one p.  Which p belong
+// to which of a wave's four fragments is chosen so that a lane's results of the four are
+// neighbours, and those of lanes that follow each other are too.  A CU writes such runs
+// four times as fast as 16-byte pieces of as many rows as it has lanes (141 and 35 GB/s),
+// and all of an output is written at a tile's end.
 #include <type_traits>
 
 #include "moonep_internal.h"
@@ -28,7 +31,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define LDS __attribute__((address_space(3)))
 
-constexpr int kBK = 64;                    // k elements of a step: 128 bytes, a cache line
 constexpr int kMaxSegs = 2 * MOONEP_MAX_E + MOONEP_MAX_R;
 constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: reads as zero
 constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
@@ -105,17 +107,29 @@ __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to)
 // ---------------------------------------------------------------------------------------
 // operand tiles in LDS
 // ---------------------------------------------------------------------------------------
-// A step's tile holds kBK k of R rows (of P or Q).  Two forms:
-//   KC  memory is contiguous along k: LDS rows of 64 k (128 bytes), the 16-byte chunk c of
-//       row r at chunk c ^ (r & 7): the 16 lanes that read at once hit different banks;
-//   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, the
-//       32-byte unit u of row k at u ^ (k & 3 | (k >> 3 & 1) << 2), read transposed.
+// A step's tile holds BK k of R rows (of P or Q), 64 or 32.  Two forms:
+//   KC  memory is contiguous along k: LDS rows of BK k, 16-byte chunk c of row r in the
+//       place of chunk c ^ swz(r);
+//   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, read
+//       transposed.  A fragment of Q is 16 neighbours, and 32-byte unit u of row k is in the
+//       place of u ^ (k & 3 | (k >> 3 & 1) << 2).  A fragment f of P is every fourth run of
+//       four: runs f, f + 4, f + 8 and f + 12 of 64 elements; 16-byte chunk c is in the
+//       place of c ^ (k & 1 | (k & 2) << 2): two lanes to a bank, the best that can be where
+//       only half of each 16 bytes is read.
 // Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
 // global address, since a wave's load fills 1024 consecutive LDS bytes.
 
-template <int R, bool KS, int NW>
+// Of LDS row r of a KC tile, to be exclusive-ored into its chunks' places.  16 lanes of a 16-byte
+// read go at once, of rows 0-3 and 12-15 in one chunk and 4-11 in the next (or the other
+// way about); with these the 16 are in different banks.
+template <int BK>
+__device__ __forceinline__ int swz(int r) {
+  return BK == 64 ? r & 7 : -(r >> 2) & 3;
+}
+
+template <int R, bool KS, int NW, int BK, bool ISP>
 struct Operand {
-  static constexpr int kBytes = R * kBK * 2;
+  static constexpr int kBytes = R * BK * 2;
   static constexpr int kLoads = kBytes / 1024 / NW;
   static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes);
   uint32_t voff[kLoads];
@@ -130,10 +144,11 @@ struct Operand {
   // KC: rowoff(r) is the byte offset of LDS row r in memory, or kOob
   template <class F>
   __device__ __forceinline__ void init_kc(int wave, int lane, F rowoff) {
-    const int c = (lane & 7) ^ (lane >> 3);
+    constexpr int kChunks = BK / 8;            // of an LDS row
+    const int r = lane / kChunks, c = (lane % kChunks) ^ swz<BK>(r);
     kc = c * 8;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * 8 + (lane >> 3)) + c * 16;
+    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * (64 / kChunks) + r) + c * 16;
   }
   // KS: columns at or past ncols read as zero
   __device__ __forceinline__ void init_ks(int wave, int lane, int ncols) {
@@ -141,8 +156,7 @@ struct Operand {
     for (int i = 0; i < kLoads; ++i) {
       const int b = (i * NW + wave) * 1024 + lane * 16;
       const int k = b / (R * 2), cp = b % (R * 2) / 16;
-      const int u = (cp >> 1) ^ ((k & 3) | ((k >> 3 & 1) << 2));
-      const int c = u * 2 + (cp & 1);
+      const int c = cp ^ (ISP ? (k & 1) | (k & 2) << 2 : ((k & 3) | (k >> 3 & 1) << 2) << 1);
       voff[i] = c * 8 < ncols ? k * ld + c * 16 : kOob;
     }
   }
@@ -150,15 +164,15 @@ struct Operand {
   // out of range, and the tile is filled with zeros.
   __device__ __forceinline__ void next() {
     const uint64_t p = reinterpret_cast<uint64_t>(at);
-    const int rows = max(min(left, kBK), 0);
+    const int rows = max(min(left, BK), 0);
     const int range = !KS ? 0x7fffffff : rows ? rows * (int)ld - (int)skip : 0;
     rs = i32x4{(int)p, (int)(p >> 32) & 0xFFFF, range, kBufferFlags};
-    if (!KS && left < kBK) {     // the last k, or none
+    if (!KS && left < BK) {     // the last k, or none
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) voff[i] |= kc >= left ? kOob : 0;
     }
-    at += KS ? (uint64_t)ld * kBK : kBK * 2;
-    left -= kBK;
+    at += KS ? (uint64_t)ld * BK : BK * 2;
+    left -= BK;
   }
   // load I of the step
   template <int I, int OFF>
@@ -167,28 +181,40 @@ struct Operand {
   }
 };
 
-// Fragment f (16 rows from row0 on), k from kk * 32 on, of a tile.
-template <int R, bool KS>
-__device__ __forceinline__ bf16x8 fragment(const char* tile, int row0, int f, int kk, int lane) {
+// `v`, of which the compiler cannot know before: what is computed of it stays where it is
+// used, and not in registers that the products need.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// This lane's part of the LDS addresses of the fragments from row0 (a multiple of what the wave
+// takes) on, and fragment f (16 rows), k from kk * 32 on, of the tile that `at` adds to it.
+template <int R, bool KS, int BK, bool ISP>
+__device__ __forceinline__ int fragment_lane(int row0, int lane) {
+  if constexpr (!KS) return (row0 + (lane & 15)) * (BK * 2) + (((lane >> 4) ^ swz<BK>(lane & 15)) << 4);
+  const int g = lane >> 4, j = (lane & 15) >> 2, k = (g * 8 + j) * (R * 2);
+  if constexpr (ISP) return k + (((row0 / 8 + (lane & 3) * 2) ^ ((j & 1) | (j & 2) << 2)) << 4);
+  return k + (((row0 / 16) ^ j ^ ((g & 1) << 2)) << 5) + (lane & 3) * 8;
+}
+template <int R, bool KS, int BK, bool ISP>
+__device__ __forceinline__ bf16x8 fragment(int at, int f, int kk) {
   if constexpr (!KS) {
-    const int a = (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-    return *reinterpret_cast<const bf16x8*>(tile + row0 * 128 + (a ^ (kk << 6)) + f * 2048);
+    return *(const LDS bf16x8*)((at ^ (kk << 6)) + f * (BK * 32));
   } else {
-    const int g = lane >> 4, j = (lane & 15) >> 2;
-    const int sw = j | ((g & 1) << 2);
-    const int a = (g * 8 + j) * (R * 2) + (((row0 / 16 + f) ^ sw) << 5) + (lane & 3) * 8 + kk * 64 * R;
+    const int x = (ISP ? (at ^ (f >> 1) << 4) + (f & 1) * 8 : at ^ (f << 5)) + kk * 64 * R;
     union { s16x4 h[2]; bf16x8 v; } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a));
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(tile + a + 4 * R * 2));
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)x);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(x + 4 * R * 2));
     return u.v;
   }
 }
 
-// Inside a block of 32 rows of a KC operand P, LDS row f*16 + g*4 + i holds row
-// g*8 + f*4 + i: a lane's results of two fragments are then 8 consecutive ones.
-__device__ __forceinline__ int p_perm(int r) {
-  return (r & ~31) | ((r >> 2 & 3) << 3) | ((r >> 4 & 1) << 2) | (r & 3);
-}
+// Row f * 16 + c of 64 LDS rows of a KC operand P holds row c * 4 + f of memory: lane c's
+// results of the four fragments are neighbours.  With gate and up rows in turn, the first
+// two fragments hold gate rows c * 2 + f, the others the same rows of up.
+__device__ __forceinline__ int p_row(int r) { return (r & ~63) | (r & 15) << 2 | (r >> 4 & 3); }
+__device__ __forceinline__ int p_row_pair(int r) { return (r >> 6) * 32 + ((r & 15) << 1 | (r >> 4 & 1)); }
 
 template <int PF, int QF>
 __device__ __forceinline__ void clear(f32x4 (&acc)[PF][QF]) {
@@ -228,6 +254,10 @@ __device__ __forceinline__ void arrive() {
   asm volatile("" ::: "memory");
 }
 
+// The wave's own reads from memory have arrived: said here, the compiler does not wait for them
+// later, when the next tile's loads would be waited for with them.
+__device__ __forceinline__ void settled() { __builtin_amdgcn_s_waitcnt(wait_vm_lds(0)); }
+
 template <int N, class F>
 __device__ __forceinline__ void times(F f) {
   if constexpr (N > 0) {
@@ -236,40 +266,42 @@ __device__ __forceinline__ void times(F f) {
   }
 }
 
-// A tile's geometry: BP x BQ results by WP x WQ waves; LDS holds the tiles of NB steps of P
-// and NB - 1 of Q.
-template <int BP_, int BQ_, int WP_, int WQ_, int NB_>
+// A tile's geometry: BP x BQ results by WP x WQ waves, in steps of BK k; LDS holds the tiles of
+// NB steps of P and NB - 1 of Q.
+template <int BP_, int BQ_, int WP_, int WQ_, int BK_, int NB_>
 struct Geometry {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NB = NB_, NW = WP * WQ;
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, BK = BK_, NB = NB_, NW = WP * WQ;
   static constexpr int PF = BP / WP / 16, QF = BQ / WQ / 16;
 };
 
-// The products of one tile after another.  Each step is two matrix instructions deep: while
-// its first half is multiplied out of registers, the second is read from LDS into others;
-// then every wave has read the whole tile, and while the second half is multiplied, the
-// first half of the next step is read, and the tiles of Q's step NB - 1 and P's step NB
-// further on start to load over the ones just read.  One barrier a step.  Each half is
-// cut into parts that start a share of the loads, then spread a share of the LDS reads
-// among their matrix instructions.  begin() starts a tile's first loads: it is called before
-// the results of the tile before are written, which hides them.
+// The products of one tile after another.  A step is one or two halves, each a matrix
+// instruction (32 k) deep.  While a half is multiplied out of registers, the next is read
+// from LDS into others.  When a step's last half is to be multiplied, every wave has read the
+// whole tile: then the tiles of Q's step NB - 1 and P's step NB further on start to load
+// over it, and the half that is read is the next step's first.  One barrier a step.  Each
+// half is cut into parts that start a share of the loads, then spread a share of the LDS
+// reads among their matrix instructions.  begin() starts a tile's first loads: it is called
+// before the results of the tile before are written, which hides them.
 template <class G, bool KSP, bool KSQ>
 struct Pipe {
-  using OpP = Operand<G::BP, KSP, G::NW>;
-  using OpQ = Operand<G::BQ, KSQ, G::NW>;
-  static constexpr int PF = G::PF, QF = G::QF, NB = G::NB;
+  static constexpr int BK = G::BK, PF = G::PF, QF = G::QF, NB = G::NB;
+  using OpP = Operand<G::BP, KSP, G::NW, BK, true>;
+  using OpQ = Operand<G::BQ, KSQ, G::NW, BK, false>;
   static constexpr int kP = OpP::kBytes, kQ = OpQ::kBytes, kLP = OpP::kLoads, kLQ = OpQ::kLoads;
   static constexpr int kQ0 = NB * kP, kLds = NB * kP + (NB - 1) * kQ;
   static constexpr int kParts = QF >= 4 ? 4 : QF, kM = PF * QF / kParts, kF = PF + QF;
+  static_assert((BK == 32 || BK == 64) && PF == 4);
   static_assert(QF % kParts == 0 && (NB - 1) * kLP + (NB - 2) * kLQ < 64 && kLds <= 160 * 1024);
-  char* smem;
   uint32_t lds;                   // this wave's first LDS byte of a load
-  int wave, lane, p0, q0;
+  int lane_p, lane_q;             // this lane's first LDS byte of a fragment
   OpP P;
   OpQ Q;
 
-  __device__ __forceinline__ Pipe(char* smem_, int wave_, int lane_)
-      : smem(smem_), wave(wave_), lane(lane_), p0(wave_ % G::WP * PF * 16), q0(wave_ / G::WP * QF * 16) {
-    lds = uni((int)(uint32_t)(uintptr_t)(LDS char*)smem + wave * 1024);
+  __device__ __forceinline__ Pipe(char* smem, int wave, int lane) {
+    const int at = (int)(uint32_t)(uintptr_t)(LDS char*)smem;
+    lds = uni(at + wave * 1024);
+    lane_p = at + fragment_lane<G::BP, KSP, BK, true>(wave % G::WP * PF * 16, lane);
+    lane_q = at + fragment_lane<G::BQ, KSQ, BK, false>(wave / G::WP * QF * 16, lane);
   }
 
   template <class FP, class FQ>
@@ -291,14 +323,15 @@ struct Pipe {
   __device__ __forceinline__ void steps(int nk, int live, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
     bf16x8 a[2][PF], b[2][QF];
 #pragma unroll
-    for (int p = 0; p < PF; ++p) a[0][p] = fragment<G::BP, KSP>(smem, p0, p, 0, lane);
+    for (int p = 0; p < PF; ++p) a[0][p] = fragment<G::BP, KSP, BK, true>(lane_p, p, 0);
 #pragma unroll
-    for (int q = 0; q < QF; ++q) b[0][q] = fragment<G::BQ, KSQ>(smem + kQ0, q0, q, 0, lane);
+    for (int q = 0; q < QF; ++q) b[0][q] = fragment<G::BQ, KSQ, BK, false>(lane_q + kQ0, q, 0);
     int cp = 0, cq = kQ0;         // this step's tiles
-    for (int i = 0; i < nk; ++i) {
-      const int np = cp == (NB - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NB - 2) * kQ ? kQ0 : cq + kQ;
+    for (int i = 0; i < nk; i += 64 / BK) {
       times<2>([&](auto h) {
-        if constexpr (h == 1) {
+        constexpr bool kLast = BK == 32 || h == 1;
+        const int np = cp == (NB - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NB - 2) * kQ ? kQ0 : cq + kQ;
+        if constexpr (kLast) {
           before_q();
           Q.next();
           before_p();
@@ -306,25 +339,24 @@ struct Pipe {
           arrive<kLP + (NB - 3) * (kLP + kLQ)>();
         }
         const uint32_t top = lds + cp, toq = lds + cq;
-        const char* tp = smem + (h ? np : cp);
-        const char* tq = smem + (h ? nq : cq);
+        const int tp = here(lane_p + (kLast ? np : cp)), tq = here(lane_q + (kLast ? nq : cq));
         times<kParts>([&](auto c) {
           times<kLP + kLQ>([&](auto j) {
-            if constexpr (h == 1 && j * kParts / (kLP + kLQ) == c) {
+            if constexpr (kLast && j * kParts / (kLP + kLQ) == c) {
               if constexpr (j < kLQ) Q.template load<j, 0>(toq);
               else P.template load<j - kLQ, 0>(top);
             }
           });
           times<kF>([&](auto f) {
             if constexpr (f * kParts / kF == c) {
-              if constexpr (f < PF) a[h ^ 1][f] = fragment<G::BP, KSP>(tp, p0, f, h ^ 1, lane);
-              else b[h ^ 1][f - PF] = fragment<G::BQ, KSQ>(tq, q0, f - PF, h ^ 1, lane);
+              if constexpr (f < PF) a[h ^ 1][f] = fragment<G::BP, KSP, BK, true>(tp, f, !kLast);
+              else b[h ^ 1][f - PF] = fragment<G::BQ, KSQ, BK, false>(tq, f - PF, !kLast);
             }
           });
           if (ALL || c * (QF / kParts) * 16 < live)
             times<kM>([&](auto m) {
               constexpr int p = m % PF, q = c * (QF / kParts) + m / PF;
-              acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[h][p], b[h][q], acc[p][q], 0, 0, 0);
+              acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[h][q], a[h][p], acc[p][q], 0, 0, 0);
             });
           if constexpr (ALL)
             times<kM>([&](auto) {
@@ -333,9 +365,11 @@ struct Pipe {
             });
           __builtin_amdgcn_sched_barrier(0);
         });
+        if constexpr (kLast) {
+          cp = np;
+          cq = nq;
+        }
       });
-      cp = np;
-      cq = nq;
     }
   }
 
@@ -346,6 +380,11 @@ struct Pipe {
     arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
     if (live >= QF * 16) steps<true>(nk, live, acc, before_p, before_q);
     else steps<false>(nk, live, acc, before_p, before_q);
+  }
+  template <class FP, class FQ>
+  __device__ __forceinline__ void run_all(int nk, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
+    arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
+    steps<true>(nk, 0, acc, before_p, before_q);
   }
 };
 
@@ -375,6 +414,51 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
   return z * p;
 }
 
+// Memory from a tile's first element on, by byte offsets; kOob for what is not to be touched.
+struct Window {
+  __amdgpu_buffer_rsrc_t rs;
+  template <class T>
+  __device__ __forceinline__ explicit Window(T* p)
+      : rs(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, kBufferFlags)) {}
+  __device__ __forceinline__ void store(uint32_t v, uint32_t at) const {
+    __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, 0, 0);
+  }
+  __device__ __forceinline__ void store(u32x2 v, uint32_t at) const {
+    __builtin_amdgcn_raw_buffer_store_b64(v, rs, at, 0, 0);
+  }
+  __device__ __forceinline__ void store(f32x4 v, uint32_t at) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, 0, 0);
+  }
+  __device__ __forceinline__ u32x2 load2(uint32_t at) const {
+    return __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+  }
+  __device__ __forceinline__ f32x4 load4(uint32_t at) const {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0));
+  }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float quad_move(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// This lane's results i of the four fragments, as four neighbours along p.  For KC that is
+// what they are.  For KS lane (m, e) holds p = m * 16 + f * 4 + e for f = 0 ... 3, and the
+// four lanes of a quad exchange theirs, for m * 16 + e * 4 + f.
+template <bool KS, int QF>
+__device__ __forceinline__ f32x4 neighbours(const f32x4 (&acc)[4][QF], int q, int i, int lane) {
+  const float v0 = acc[0][q][i], v1 = acc[1][q][i], v2 = acc[2][q][i], v3 = acc[3][q][i];
+  if constexpr (!KS) return f32x4{v0, v1, v2, v3};
+  const bool odd = lane & 1, high = lane & 2;
+  // every lane takes part in a move, so none is in a branch
+  const float x0 = quad_move<0xB1>(v0), x1 = quad_move<0xB1>(v1);                          // of lane ^ 1
+  const float x2 = quad_move<0xB1>(v2), x3 = quad_move<0xB1>(v3);
+  const float n0 = odd ? x1 : v0, n1 = odd ? v1 : x0, n2 = odd ? x3 : v2, n3 = odd ? v3 : x2;
+  const float y0 = quad_move<0x4E>(n0), y1 = quad_move<0x4E>(n1);                          // of lane ^ 2
+  const float y2 = quad_move<0x4E>(n2), y3 = quad_move<0x4E>(n3);
+  return f32x4{high ? y2 : n0, high ? y3 : n1, high ? n2 : y0, high ? n3 : y1};
+}
+
 // ---------------------------------------------------------------------------------------
 // the row products: forward, and the rows' gradient
 // ---------------------------------------------------------------------------------------
@@ -390,7 +474,7 @@ __device__ __forceinline__ int wave_sums(int v, int lane) {
 }
 
 template <int OP, class G>
-__global__ __launch_bounds__(64 * G::NW, 1) void rows_kernel(const FfnArgs a) {
+__global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
   constexpr int BP = G::BP, BQ = G::BQ, WP = G::WP, PF = G::PF, QF = G::QF;
   constexpr bool KSP = OP == BWD1 || OP == BWD2;
@@ -408,7 +492,7 @@ __global__ __launch_bounds__(64 * G::NW, 1) void rows_kernel(const FfnArgs a) {
   const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
   const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
   const int nt = (N + BN - 1) / BN;
-  const int nk = (K + kBK - 1) / kBK;
+  const int nk = (K + G::BK - 1) / G::BK;
 
   // Lane l sums the row tiles of segments [l * per, l * per + per); a tile is then found by
   // comparing its number with all sums at once, in each wave on its own: no LDS, no
@@ -463,10 +547,10 @@ __global__ __launch_bounds__(64 * G::NW, 1) void rows_kernel(const FfnArgs a) {
       P.at = reinterpret_cast<const char*>(W) + (int64_t)n0 * P.ld;
       P.init_kc(wave, lane, [&](int r) -> uint32_t {
         if (PAIR) {
-          const int c = (r >> 6) * 32 + p_perm(r & 31);
+          const int c = p_row_pair(r);
           return n0 + c < N ? (uint32_t)(c + (r >> 5 & 1) * a.I) * P.ld : kOob;
         }
-        const int c = p_perm(r);
+        const int c = p_row(r);
         return n0 + c < N ? (uint32_t)c * P.ld : kOob;
       });
     } else {
@@ -491,72 +575,55 @@ __global__ __launch_bounds__(64 * G::NW, 1) void rows_kernel(const FfnArgs a) {
     const bool idle = tn0 + (PAIR ? wp * PF * 8 : wp * PF * 16) >= N;     // no columns for this wave
     pipe.run(nk, idle ? 0 : tq - wq * QF * 16, acc, none, none);
     have = set_up(round);
+    settled();
     if (have) pipe.begin(none, none);
 
-    const int g = lane >> 4;
+    // what the results' places are made of is worked out here, not kept during the products
+    const int ln = here(lane);
+    const int ldo = OP == BWD1 ? 2 * N : N;                               // elements of an output row
+    const int64_t o0 = (int64_t)trow * ldo + tn0;
+    const Window out(a.out + o0), gu(OP == FWD1 ? a.gu_out + 2 * o0 - tn0 : a.gu_in + o0);
+    const bool save = OP == FWD1 && a.gu_out;
+    const int c = wp * BN / WP + (ln & 15) * (PAIR ? 2 : 4);
+    const bool in = tn0 + c < N;
 #pragma unroll
     for (int q = 0; q < QF; ++q) {
-      const int r = wq * QF * 16 + q * 16 + (lane & 15);
-      if (r >= tq) continue;
-      const int64_t row = trow + r;
-      if constexpr (OP == FWD1) {
 #pragma unroll
-        for (int pb4 = 0; pb4 < PF; pb4 += 4) {
-          const int c = tn0 + (wp * PF + pb4) * 8 + g * 8;       // 64 P rows give 32 columns
-          if (c >= N) continue;
-          u32x4 h, vg, vu;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int f = e >> 1, i = (e & 1) * 2;
-            const float g0 = acc[pb4 + f][q][i], g1 = acc[pb4 + f][q][i + 1];
-            const float u0 = acc[pb4 + 2 + f][q][i], u1 = acc[pb4 + 2 + f][q][i + 1];
-            float sl0, sl1;
-            h[e] = bf2(act_of(g0, a.act, &sl0) * u0, act_of(g1, a.act, &sl1) * u1);
-            vg[e] = bf2(g0, g1);
-            vu[e] = bf2(u0, u1);
+      for (int i = 0; i < 4; ++i) {
+        const int r = (wq * QF + q) * 16 + (ln >> 4) * 4 + i;
+        const bool here_too = in && r < tq;
+        const uint32_t at = here_too ? (uint32_t)(r * ldo + c) * 2 : kOob;
+        if constexpr (OP == FWD1) {
+          const float g0 = acc[0][q][i], g1 = acc[1][q][i], u0 = acc[2][q][i], u1 = acc[3][q][i];
+          float s0, s1;
+          out.store(bf2(act_of(g0, a.act, &s0) * u0, act_of(g1, a.act, &s1) * u1), at);
+          if (save) {
+            const uint32_t at2 = here_too ? (uint32_t)(r * 2 * N + c) * 2 : kOob;
+            gu.store(bf2(g0, g1), at2);
+            gu.store(bf2(u0, u1), here_too ? at2 + N * 2 : kOob);
           }
-          *reinterpret_cast<u32x4*>(a.out + row * N + c) = h;
-          if (a.gu_out) {
-            *reinterpret_cast<u32x4*>(a.gu_out + row * 2 * N + c) = vg;
-            *reinterpret_cast<u32x4*>(a.gu_out + row * 2 * N + N + c) = vu;
-          }
-        }
-      } else if constexpr (OP == FWD2) {
+        } else {
+          const f32x4 d = neighbours<KSP>(acc, q, i, ln);
+          if constexpr (OP == BWD1) {
+            const uint32_t at_up = here_too ? at + N * 2 : kOob;
+            const u32x2 vg = gu.load2(at), vu = gu.load2(at_up);
+            float gg[4], gv[4];
 #pragma unroll
-        for (int p = 0; p < PF; p += 2) {
-          const int c = tn0 + (wp * PF + p) * 16 + g * 8;
-          if (c >= N) continue;
-          u32x4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = bf2(acc[p + (e >> 1)][q][(e & 1) * 2], acc[p + (e >> 1)][q][(e & 1) * 2 + 1]);
-          *reinterpret_cast<u32x4*>(a.out + row * N + c) = v;
-        }
-      } else {
-#pragma unroll
-        for (int p = 0; p < PF; ++p) {
-          const int c = tn0 + (wp * PF + p) * 16 + g * 4;
-          if (c >= N) continue;
-          const f32x4 d = acc[p][q];
-          if constexpr (OP == BWD2) {
-            *reinterpret_cast<u32x2*>(a.out + row * N + c) = u32x2{bf2(d[0], d[1]), bf2(d[2], d[3])};
-          } else {
-            const u32x2 vg = *reinterpret_cast<const u32x2*>(a.gu_in + row * 2 * N + c);
-            const u32x2 vu = *reinterpret_cast<const u32x2*>(a.gu_in + row * 2 * N + N + c);
-            float gg[4], gu[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float z = i & 1 ? hi(vg[i >> 1]) : lo(vg[i >> 1]);
-              const float u = i & 1 ? hi(vu[i >> 1]) : lo(vu[i >> 1]);
+            for (int e = 0; e < 4; ++e) {
+              const float z = e & 1 ? hi(vg[e >> 1]) : lo(vg[e >> 1]);
+              const float u = e & 1 ? hi(vu[e >> 1]) : lo(vu[e >> 1]);
               float slope;
-              gu[i] = d[i] * act_of(z, a.act, &slope);
-              gg[i] = d[i] * u * slope;
+              gv[e] = d[e] * act_of(z, a.act, &slope);
+              gg[e] = d[e] * u * slope;
             }
-            *reinterpret_cast<u32x2*>(a.out + row * 2 * N + c) = u32x2{bf2(gg[0], gg[1]), bf2(gg[2], gg[3])};
-            *reinterpret_cast<u32x2*>(a.out + row * 2 * N + N + c) = u32x2{bf2(gu[0], gu[1]), bf2(gu[2], gu[3])};
+            out.store(u32x2{bf2(gg[0], gg[1]), bf2(gg[2], gg[3])}, at);
+            out.store(u32x2{bf2(gv[0], gv[1]), bf2(gv[2], gv[3])}, at_up);
+          } else {
+            out.store(u32x2{bf2(d[0], d[1]), bf2(d[2], d[3])}, at);
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);         // or all results are worked on at once, and spill
     }
   }
 #endif
@@ -579,7 +646,7 @@ struct GradArgs {
 };
 
 template <class G>
-__global__ __launch_bounds__(64 * G::NW, 1) void grad_kernel(const GradArgs a) {
+__global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int BP = G::BP, BQ = G::BQ, WP = G::WP, PF = G::PF, QF = G::QF;
   using Tiles = Pipe<G, true, true>;
@@ -614,8 +681,7 @@ __global__ __launch_bounds__(64 * G::NW, 1) void grad_kernel(const GradArgs a) {
       const Seg fb = load_seg(plan, s, s.E + f, np);
       ++f;
       if (uni(fb.w) == target && uni(fb.n) > 0) start(side, src, uni(fb.row0), uni(fb.n));
-      // here, and not at some later use on the common path, where it would drain the ring
-      __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
+      settled();
     }
   };
   auto walk_p = [&] { walk(P, psrc, fp); };
@@ -665,10 +731,10 @@ __global__ __launch_bounds__(64 * G::NW, 1) void grad_kernel(const GradArgs a) {
       Q.init_ks(wave, lane, qcols - q0);
       start(P, psrc, uni(seg.row0), uni(seg.n));
       start(Q, qsrc, uni(seg.row0), uni(seg.n));
-      steps = (P.left + kBK - 1) / kBK;
+      steps = (P.left + G::BK - 1) / G::BK;
       for (int f = fp; f < fend; ++f) {
         const Seg fb = load_seg(plan, s, s.E + f, np);
-        if (uni(fb.w) == target) steps += (uni(fb.n) + kBK - 1) / kBK;
+        if (uni(fb.w) == target) steps += (uni(fb.n) + G::BK - 1) / G::BK;
       }
       if (steps == 0 && a.accumulate) continue;
       return true;
@@ -683,30 +749,33 @@ __global__ __launch_bounds__(64 * G::NW, 1) void grad_kernel(const GradArgs a) {
     const int tp0 = p0, tq0 = q0, tpc = pcols, tqc = qcols;
     const bool add = a.accumulate && target < s.E;
     float* const tout = out;
-    const bool idle = tp0 + wp * PF * 16 >= tpc;
-    if (steps) pipe.run(steps, idle ? 0 : tqc - tq0 - wq * QF * 16, acc, walk_p, walk_q);
+    if (steps) pipe.run_all(steps, acc, walk_p, walk_q);
     have = set_up();
+    settled();
     if (have && steps) pipe.begin(walk_p, walk_q);
 
+    const Window o(tout + (int64_t)tq0 * tpc + tp0);
+    const int ln = here(lane), c = wp * 64 + (ln & 15) * 4;
+    const bool in = tp0 + c < tpc;
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
-      const int r = tq0 + (wq * QF + f) * 16 + (lane & 15);
-      if (r >= tqc) continue;
 #pragma unroll
-      for (int p = 0; p < PF; ++p) {
-        const int c = tp0 + (wp * PF + p) * 16 + (lane >> 4) * 4;
-        if (c >= tpc) continue;
-        f32x4* o = reinterpret_cast<f32x4*>(tout + (int64_t)r * tpc + c);
-        *o = add ? *o + acc[p][f] : acc[p][f];
+      for (int i = 0; i < 4; ++i) {
+        const int r = (wq * QF + f) * 16 + (ln >> 4) * 4 + i;
+        const uint32_t at = in && tq0 + r < tqc ? (uint32_t)(r * tpc + c) * 4 : kOob;
+        f32x4 d = neighbours<true>(acc, f, i, ln);
+        if (add) d = d + o.load4(at);
+        o.store(d, at);
       }
+      __builtin_amdgcn_sched_barrier(0);         // or all results are worked on at once, and spill
     }
   }
 #endif
 }
 
-using Large = Geometry<256, 256, 4, 2, 3>;
-using Medium = Geometry<128, 64, 2, 2, 3>;
-using Small = Geometry<128, 32, 2, 2, 4>;
+using Large = Geometry<256, 256, 4, 2, 64, 3>;
+using Medium = Geometry<128, 64, 2, 2, 64, 3>;
+using Small = Geometry<128, 32, 2, 2, 64, 4>;
 
 template <int OP, class G>
 hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
@@ -817,7 +886,7 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
   a.recv = recv; a.g_y = g_y; a.h = h; a.g_gu = g_gu;
   a.home = home_grad; a.rep = rep_grad; a.G_el = G_el;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((grad_kernel<Large>), dim3(kCus), dim3(512), 0, stream, a);
+  hipLaunchKernelGGL((grad_kernel<Large>), dim3(kCus), dim3(64 * Large::NW), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
