@@ -36,6 +36,8 @@ constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: 
 constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
 constexpr int kCus = 256;
 
+constexpr int BK = 64;                     // k of a step
+
 enum Op { FWD1, FWD2, BWD1, BWD2 };
 
 struct FfnArgs {
@@ -62,17 +64,18 @@ struct Seg {
 
 // Segment i of the plan: the E home groups, then the pieces.  Whatever the blob holds, the
 // rows stay inside the buffer and the weights inside their tables.
-__device__ __forceinline__ Seg load_seg(const int32_t* plan, const moonep_sizes& s, int i, int np) {
+template <class Load>
+__device__ __forceinline__ Seg read_seg(const int32_t* plan, const moonep_sizes& s, int i, int np, Load load) {
   Seg g{0, 0, 0};
   if (i < s.E) {
-    g.n = plan[s.o_keep + i];
-    g.row0 = plan[s.o_home_row + i];
+    g.n = load(plan + s.o_keep + i);
+    g.row0 = load(plan + s.o_home_row + i);
     g.w = i;
   } else if (i - s.E < np) {
     const int32_t* pc = plan + s.o_pieces + (int64_t)(i - s.E) * kPieceInts;
-    const int e = pc[P_E], r = pc[P_R], slot = pc[P_SLOT];
-    g.n = pc[P_CNT];
-    g.row0 = pc[P_ROW0];
+    const int e = load(pc + P_E), r = load(pc + P_R), slot = load(pc + P_SLOT);
+    g.n = load(pc + P_CNT);
+    g.row0 = load(pc + P_ROW0);
     if (slot >= 0) {
       g.w = s.E + r * s.slots + slot;
       if (slot >= s.slots || (unsigned)r >= (unsigned)s.R) g.n = 0;
@@ -87,9 +90,24 @@ __device__ __forceinline__ Seg load_seg(const int32_t* plan, const moonep_sizes&
   return g;
 }
 
+__device__ __forceinline__ Seg load_seg(const int32_t* plan, const moonep_sizes& s, int i, int np) {
+  return read_seg(plan, s, i, np, [](const int32_t* p) { return *p; });
+}
+
 __device__ __forceinline__ int piece_count(const int32_t* plan, const moonep_sizes& s) {
   if (plan[s.o_hdr + H_STATUS] != 0) return 0;
   return min(max(plan[s.o_hdr + H_NPIECES], 0), s.P_max);
+}
+
+// A word of the plan through the scalar cache, at a uniform address: waited for apart from the
+// loads into LDS.
+__device__ __forceinline__ int scalar(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+
+// load_seg for a uniform index.
+__device__ __forceinline__ Seg scalar_seg(const int32_t* plan, const moonep_sizes& s, int i, int np) {
+  return read_seg(plan, s, i, np, [](const int32_t* p) { return scalar(p); });
 }
 
 // 16 bytes a lane from the buffer straight into LDS, to `to` + OFF + lane * 16.  In assembly:
@@ -107,9 +125,9 @@ __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to)
 // ---------------------------------------------------------------------------------------
 // operand tiles in LDS
 // ---------------------------------------------------------------------------------------
-// A step's tile holds BK k of R rows (of P or Q), 64 or 32.  Two forms:
-//   KC  memory is contiguous along k: LDS rows of BK k, 16-byte chunk c of row r in the
-//       place of chunk c ^ swz(r);
+// A step's tile holds BK k of R rows (of P or Q): 64 k are a cache line.  Two forms:
+//   KC  memory is contiguous along k: LDS rows of 64 k, 16-byte chunk c of row r in the place
+//       of chunk c ^ (r & 7): the 16 lanes that read at once hit different banks.
 //   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, read
 //       transposed.  A fragment of Q is 16 neighbours, and 32-byte unit u of row k is in the
 //       place of u ^ (k & 3 | (k >> 3 & 1) << 2).  A fragment f of P is every fourth run of
@@ -119,24 +137,17 @@ __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to)
 // Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
 // global address, since a wave's load fills 1024 consecutive LDS bytes.
 
-// Of LDS row r of a KC tile, to be exclusive-ored into its chunks' places.  16 lanes of a 16-byte
-// read go at once, of rows 0-3 and 12-15 in one chunk and 4-11 in the next (or the other
-// way about); with these the 16 are in different banks.
-template <int BK>
-__device__ __forceinline__ int swz(int r) {
-  return BK == 64 ? r & 7 : -(r >> 2) & 3;
-}
-
-template <int R, bool KS, int NW, int BK, bool ISP>
+template <int R, bool KS, int NW, bool ISP>
 struct Operand {
   static constexpr int kBytes = R * BK * 2;
   static constexpr int kLoads = kBytes / 1024 / NW;
   static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes);
   uint32_t voff[kLoads];
   int kc;                        // KC: this lane's first k inside a step
-  // the next step to load: its address and the k left from there (uniform)
+  // the next step to load: its address, the k left from there, and the steps of this tile
+  // from there on (uniform)
   const char* at;
-  int left;
+  int left, todo;
   uint32_t ld;                   // bytes of a row in memory
   uint32_t skip;                 // KS: bytes of the row before `at`
   i32x4 rs;
@@ -144,11 +155,10 @@ struct Operand {
   // KC: rowoff(r) is the byte offset of LDS row r in memory, or kOob
   template <class F>
   __device__ __forceinline__ void init_kc(int wave, int lane, F rowoff) {
-    constexpr int kChunks = BK / 8;            // of an LDS row
-    const int r = lane / kChunks, c = (lane % kChunks) ^ swz<BK>(r);
+    const int r = lane >> 3, c = (lane & 7) ^ r;
     kc = c * 8;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * (64 / kChunks) + r) + c * 16;
+    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * 8 + r) + c * 16;
   }
   // KS: columns at or past ncols read as zero
   __device__ __forceinline__ void init_ks(int wave, int lane, int ncols) {
@@ -173,6 +183,7 @@ struct Operand {
     }
     at += KS ? (uint64_t)ld * BK : BK * 2;
     left -= BK;
+    --todo;
   }
   // load I of the step
   template <int I, int OFF>
@@ -190,17 +201,17 @@ __device__ __forceinline__ int here(int v) {
 
 // This lane's part of the LDS addresses of the fragments from row0 (a multiple of what the wave
 // takes) on, and fragment f (16 rows), k from kk * 32 on, of the tile that `at` adds to it.
-template <int R, bool KS, int BK, bool ISP>
+template <int R, bool KS, bool ISP>
 __device__ __forceinline__ int fragment_lane(int row0, int lane) {
-  if constexpr (!KS) return (row0 + (lane & 15)) * (BK * 2) + (((lane >> 4) ^ swz<BK>(lane & 15)) << 4);
+  if constexpr (!KS) return (row0 + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
   const int g = lane >> 4, j = (lane & 15) >> 2, k = (g * 8 + j) * (R * 2);
   if constexpr (ISP) return k + (((row0 / 8 + (lane & 3) * 2) ^ ((j & 1) | (j & 2) << 2)) << 4);
   return k + (((row0 / 16) ^ j ^ ((g & 1) << 2)) << 5) + (lane & 3) * 8;
 }
-template <int R, bool KS, int BK, bool ISP>
+template <int R, bool KS, bool ISP>
 __device__ __forceinline__ bf16x8 fragment(int at, int f, int kk) {
   if constexpr (!KS) {
-    return *(const LDS bf16x8*)((at ^ (kk << 6)) + f * (BK * 32));
+    return *(const LDS bf16x8*)((at ^ (kk << 6)) + f * 2048);
   } else {
     const int x = (ISP ? (at ^ (f >> 1) << 4) + (f & 1) * 8 : at ^ (f << 5)) + kk * 64 * R;
     union { s16x4 h[2]; bf16x8 v; } u;
@@ -266,77 +277,89 @@ __device__ __forceinline__ void times(F f) {
   }
 }
 
-// A tile's geometry: BP x BQ results by WP x WQ waves, in steps of BK k; LDS holds the tiles of
-// NB steps of P and NB - 1 of Q.
-template <int BP_, int BQ_, int WP_, int WQ_, int BK_, int NB_>
+// A tile's geometry: BP x BQ results by WP x WQ waves; LDS holds the tiles of NB steps of P and
+// NB - 1 of Q.
+template <int BP_, int BQ_, int WP_, int WQ_, int NB_>
 struct Geometry {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, BK = BK_, NB = NB_, NW = WP * WQ;
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NB = NB_, NW = WP * WQ;
   static constexpr int PF = BP / WP / 16, QF = BQ / WQ / 16;
 };
 
-// The products of one tile after another.  A step is one or two halves, each a matrix
-// instruction (32 k) deep.  While a half is multiplied out of registers, the next is read
-// from LDS into others.  When a step's last half is to be multiplied, every wave has read the
-// whole tile: then the tiles of Q's step NB - 1 and P's step NB further on start to load
-// over it, and the half that is read is the next step's first.  One barrier a step.  Each
-// half is cut into parts that start a share of the loads, then spread a share of the LDS
-// reads among their matrix instructions.  begin() starts a tile's first loads: it is called
-// before the results of the tile before are written, which hides them.
+// The products of one tile after another, without a break between them.  A step is two halves,
+// each a matrix instruction (32 k) deep.  While a half is multiplied out of
+// registers, the next is read from LDS into others.  When a step's last half is to be
+// multiplied, every wave has read the whole tile: then the tiles of Q's step NB - 1 and P's
+// step NB further on start to load over it, and the half that is read is the next step's
+// first.  Past a tile's end these are the next tile's steps: more_p() and more_q() turn their
+// side to it, or fill with zeros.  One barrier a step.  Each half is cut into parts that
+// start a share of the loads, then spread a share of the LDS reads among their matrix
+// instructions.
 template <class G, bool KSP, bool KSQ>
 struct Pipe {
-  static constexpr int BK = G::BK, PF = G::PF, QF = G::QF, NB = G::NB;
-  using OpP = Operand<G::BP, KSP, G::NW, BK, true>;
-  using OpQ = Operand<G::BQ, KSQ, G::NW, BK, false>;
+  static constexpr int PF = G::PF, QF = G::QF, NB = G::NB;
+  using OpP = Operand<G::BP, KSP, G::NW, true>;
+  using OpQ = Operand<G::BQ, KSQ, G::NW, false>;
   static constexpr int kP = OpP::kBytes, kQ = OpQ::kBytes, kLP = OpP::kLoads, kLQ = OpQ::kLoads;
   static constexpr int kQ0 = NB * kP, kLds = NB * kP + (NB - 1) * kQ;
   static constexpr int kParts = QF >= 4 ? 4 : QF, kM = PF * QF / kParts, kF = PF + QF;
-  static_assert((BK == 32 || BK == 64) && PF == 4);
-  static_assert(QF % kParts == 0 && (NB - 1) * kLP + (NB - 2) * kLQ < 64 && kLds <= 160 * 1024);
+  static constexpr int kAhead = kLP + (NB - 3) * (kLP + kLQ);   // loads after the next step's
+  static_assert(PF == 4 && QF % kParts == 0 && (NB - 1) * kLP + (NB - 2) * kLQ < 64 && kLds <= 160 * 1024);
   uint32_t lds;                   // this wave's first LDS byte of a load
   int lane_p, lane_q;             // this lane's first LDS byte of a fragment
+  int cp, cq;                     // the current step's tiles
   OpP P;
   OpQ Q;
 
-  __device__ __forceinline__ Pipe(char* smem, int wave, int lane) {
+  __device__ __forceinline__ Pipe(char* smem, int wave, int lane) : cp(0), cq(kQ0) {
     const int at = (int)(uint32_t)(uintptr_t)(LDS char*)smem;
     lds = uni(at + wave * 1024);
-    lane_p = at + fragment_lane<G::BP, KSP, BK, true>(wave % G::WP * PF * 16, lane);
-    lane_q = at + fragment_lane<G::BQ, KSQ, BK, false>(wave / G::WP * QF * 16, lane);
+    lane_p = at + fragment_lane<G::BP, KSP, true>(wave % G::WP * PF * 16, lane);
+    lane_q = at + fragment_lane<G::BQ, KSQ, false>(wave / G::WP * QF * 16, lane);
   }
 
+  // the first tile's first loads
   template <class FP, class FQ>
-  __device__ __forceinline__ void begin(FP before_p, FQ before_q) {
-    arrive<0>();                  // the tile before is read, and its loads past the end have landed
+  __device__ __forceinline__ void begin(FP more_p, FQ more_q) {
     times<NB>([&](auto i) {
-      before_p();
+      more_p();
       P.next();
       times<kLP>([&](auto j) { P.template load<j, i * kP>(lds); });
       if constexpr (i < NB - 1) {
-        before_q();
+        more_q();
         Q.next();
         times<kLQ>([&](auto j) { Q.template load<j, kQ0 + i * kQ>(lds); });
       }
     });
+    arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
   }
 
-  template <bool ALL, class FP, class FQ>
-  __device__ __forceinline__ void steps(int nk, int live, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
+  // The next `nk` steps.  `live`: how many of the wave's rows of Q are there; where they are
+  // not ALL, the matrix instructions of the rest are left out.  `younger`: at least STORES
+  // stores went out since the last step, and need not have arrived for its loads to have
+  // (memory operations are counted in order).
+  template <bool ALL, int STORES, class FP, class FQ>
+  __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[PF][QF], FP more_p,
+                                      FQ more_q) {
     bf16x8 a[2][PF], b[2][QF];
+    {
+      const int tp = here(lane_p + cp), tq = here(lane_q + cq);
 #pragma unroll
-    for (int p = 0; p < PF; ++p) a[0][p] = fragment<G::BP, KSP, BK, true>(lane_p, p, 0);
+      for (int p = 0; p < PF; ++p) a[0][p] = fragment<G::BP, KSP, true>(tp, p, 0);
 #pragma unroll
-    for (int q = 0; q < QF; ++q) b[0][q] = fragment<G::BQ, KSQ, BK, false>(lane_q + kQ0, q, 0);
-    int cp = 0, cq = kQ0;         // this step's tiles
-    for (int i = 0; i < nk; i += 64 / BK) {
+      for (int q = 0; q < QF; ++q) b[0][q] = fragment<G::BQ, KSQ, false>(tq, q, 0);
+    }
+    for (int i = 0; i < nk; ++i) {
       times<2>([&](auto h) {
-        constexpr bool kLast = BK == 32 || h == 1;
+        constexpr bool kLast = h == 1;
         const int np = cp == (NB - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NB - 2) * kQ ? kQ0 : cq + kQ;
         if constexpr (kLast) {
-          before_q();
+          more_q();
           Q.next();
-          before_p();
+          more_p();
           P.next();
-          arrive<kLP + (NB - 3) * (kLP + kLQ)>();
+          constexpr int kMore = kAhead + STORES < 63 ? kAhead + STORES : 63;
+          if (younger && i == 0) arrive<kMore>();
+          else arrive<kAhead>();
         }
         const uint32_t top = lds + cp, toq = lds + cq;
         const int tp = here(lane_p + (kLast ? np : cp)), tq = here(lane_q + (kLast ? nq : cq));
@@ -349,8 +372,8 @@ struct Pipe {
           });
           times<kF>([&](auto f) {
             if constexpr (f * kParts / kF == c) {
-              if constexpr (f < PF) a[h ^ 1][f] = fragment<G::BP, KSP, BK, true>(tp, f, !kLast);
-              else b[h ^ 1][f - PF] = fragment<G::BQ, KSQ, BK, false>(tq, f - PF, !kLast);
+              if constexpr (f < PF) a[h ^ 1][f] = fragment<G::BP, KSP, true>(tp, f, !kLast);
+              else b[h ^ 1][f - PF] = fragment<G::BQ, KSQ, false>(tq, f - PF, !kLast);
             }
           });
           if (ALL || c * (QF / kParts) * 16 < live)
@@ -371,20 +394,6 @@ struct Pipe {
         }
       });
     }
-  }
-
-  // `live`: how many of the wave's rows of Q are there.  Where they are not all, the matrix
-  // instructions of the rest are left out.
-  template <class FP, class FQ>
-  __device__ __forceinline__ void run(int nk, int live, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
-    arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
-    if (live >= QF * 16) steps<true>(nk, live, acc, before_p, before_q);
-    else steps<false>(nk, live, acc, before_p, before_q);
-  }
-  template <class FP, class FQ>
-  __device__ __forceinline__ void run_all(int nk, f32x4 (&acc)[PF][QF], FP before_p, FQ before_q) {
-    arrive<(NB - 1) * kLP + (NB - 2) * kLQ>();
-    steps<true>(nk, 0, acc, before_p, before_q);
   }
 };
 
@@ -492,11 +501,9 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
   const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
   const int nt = (N + BN - 1) / BN;
-  const int nk = (K + G::BK - 1) / G::BK;
+  const int nk = max((K + BK - 1) / BK, G::NB);      // P loads NB steps ahead, into one more tile only
 
-  // Lane l sums the row tiles of segments [l * per, l * per + per); a tile is then found by
-  // comparing its number with all sums at once, in each wave on its own: no LDS, no
-  // barrier.
+  // Lane l sums the row tiles of segments [l * per, l * per + per).
   const int per = (nseg + 63) / 64;
   int sum = 0;
   for (int j = 0; j < per; ++j) {
@@ -506,77 +513,97 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   sum = wave_sums(sum, lane);
   const int tiles = min(__builtin_amdgcn_readlane(sum, 63), a.tiles_bound) * nt;
 
-  Tiles pipe(smem, wave, lane);
-  int row0 = 0, nq = 0, n0 = 0;                 // of the tile that is set up
-  auto none = [] {};
-
-  // sets up the tile of round `round`; false where there is none
-  auto set_up = [&](int round) -> bool {
-    const int t = tile_of(round, blockIdx.x, gridDim.x);
-    if (t < 0 || t >= tiles) return false;
-    const int want = t / nt;
-    const int l = __builtin_popcountll(__ballot(sum <= want));
-    int below = l ? __builtin_amdgcn_readlane(sum, l - 1) : 0;
+  // Lane l looks up the workgroup's tile of round first + l, each wave on its own: no LDS,
+  // no barrier, and 64 rounds without a wait for memory.
+  int lane_row = -1;                            // first row, or none
+  uint32_t lane_rest = 0;                       // rows - 1, column tile, weight
+  auto look_up = [&](int first) {
+    const int t = tile_of(first + lane, blockIdx.x, gridDim.x);
+    const int want = t < 0 || t >= tiles ? 0 : t / nt;
+    int l = 0;                                  // the sums that are at most `want`
+#pragma unroll
+    for (int d = 32; d; d /= 2)
+      if (__shfl(sum, l + d - 1) <= want) l += d;
+    int below = __shfl(sum, max(l - 1, 0));
+    below = l ? below : 0;
     Seg g{0, 0, 0};
-    if (lane < per) g = load_seg(plan, a.s, l * per + lane, np);
-    const int cnt = (g.n + BQ - 1) / BQ;
-    int inc = cnt, j = 0;
-    if (per > 1) {
-      inc = wave_sums(cnt, lane);
-      j = __builtin_popcountll(__ballot(lane < per && below + inc <= want));
-      if (j >= per) return false;               // the plan changed under the call
-      below += j ? __builtin_amdgcn_readlane(inc, j - 1) : 0;
+    int mt = 0;
+    for (int j = 0; j < per; ++j) {
+      g = load_seg(plan, a.s, min(l * per + j, nseg - 1), np);
+      mt = (g.n + BQ - 1) / BQ;
+      if (below + mt > want) break;
+      below += mt;
     }
-    const int seg_row = __builtin_amdgcn_readlane(g.row0, j), n = __builtin_amdgcn_readlane(g.n, j);
-    const int w = __builtin_amdgcn_readlane(g.w, j), mt = __builtin_amdgcn_readlane(cnt, j);
-    int tm, tn;
-    if (mt <= 0) return false;
-    band(t - below * nt, mt, nt, &tm, &tn);
-    row0 = seg_row + tm * BQ;
-    nq = n - tm * BQ;
-    n0 = tn * BN;
-    if (nq <= 0 || n0 >= N) return false;
-    const uint16_t* W = w < a.s.E ? a.home_w + w * a.W_el : a.slot_w + (w - a.s.E) * a.W_el;
+    lane_row = -1;
+    const int local = t - below * nt;
+    if (t >= 0 && t < tiles && local >= 0 && local < mt * nt) {
+      int tm, tn;
+      band(local, mt, nt, &tm, &tn);
+      lane_row = g.row0 + tm * BQ;
+      lane_rest = (uint32_t)(min(g.n - tm * BQ, BQ) - 1) | (uint32_t)tn << 8 | (uint32_t)g.w << 17;
+    }
+    settled();
+  };
+  struct Tile {
+    int row, rows, n0, w;                       // rows 0: none
+  };
+  auto tile = [&](int round) -> Tile {
+    if (round && (round & 63) == 0) look_up(round);
+    const int row = __builtin_amdgcn_readlane(lane_row, round & 63);
+    const uint32_t rest = __builtin_amdgcn_readlane(lane_rest, round & 63);
+    if (row < 0) return {0, 0, 0, 0};
+    return {row, (int)(rest & 255) + 1, (int)(rest >> 8 & 511) * BN, (int)(rest >> 17)};
+  };
+  look_up(0);
+
+  Tiles pipe(smem, wave, lane);
+  auto& P = pipe.P;
+  auto& Q = pipe.Q;
+  auto start_p = [&](const Tile& t) {
+    const uint16_t* W = t.w < a.s.E ? a.home_w + t.w * a.W_el : a.slot_w + (t.w - a.s.E) * a.W_el;
     if (OP == FWD2 || OP == BWD1) W += 2ll * a.I * a.H;
-    auto& P = pipe.P;
-    auto& Q = pipe.Q;
-    P.left = Q.left = K;
+    P.left = K;
+    P.todo = nk;
     if constexpr (!KSP) {
       P.ld = K * 2;
       P.skip = 0;
-      P.at = reinterpret_cast<const char*>(W) + (int64_t)n0 * P.ld;
-      P.init_kc(wave, lane, [&](int r) -> uint32_t {
-        if (PAIR) {
-          const int c = p_row_pair(r);
-          return n0 + c < N ? (uint32_t)(c + (r >> 5 & 1) * a.I) * P.ld : kOob;
-        }
-        const int c = p_row(r);
-        return n0 + c < N ? (uint32_t)c * P.ld : kOob;
+      P.at = reinterpret_cast<const char*>(W) + (int64_t)t.n0 * P.ld;
+      P.init_kc(wave, here(lane), [&](int r) -> uint32_t {
+        const int c = PAIR ? p_row_pair(r) : p_row(r);
+        return t.n0 + c < N ? (uint32_t)(c + (PAIR ? (r >> 5 & 1) * a.I : 0)) * P.ld : kOob;
       });
     } else {
       P.ld = N * 2;
-      P.skip = n0 * 2;
+      P.skip = t.n0 * 2;
       P.at = reinterpret_cast<const char*>(W) + P.skip;
-      P.init_ks(wave, lane, N - n0);
+      P.init_ks(wave, here(lane), N - t.n0);
     }
+  };
+  auto start_q = [&](const Tile& t) {
+    Q.left = K;
+    Q.todo = nk;
     Q.ld = K * 2;
     Q.skip = 0;
-    Q.at = reinterpret_cast<const char*>(a.in) + (int64_t)row0 * Q.ld;
-    Q.init_kc(wave, lane, [&](int r) -> uint32_t { return r < nq ? r * Q.ld : kOob; });
-    return true;
+    Q.at = reinterpret_cast<const char*>(a.in) + (int64_t)t.row * Q.ld;
+    Q.init_kc(wave, here(lane), [&](int r) -> uint32_t { return r < t.rows ? r * Q.ld : kOob; });
   };
 
-  bool have = set_up(0);
-  if (have) pipe.begin(none, none);
-  for (int round = 1; have; ++round) {
+  Tile cur = tile(0), nxt = tile(1);
+  if (!cur.rows) return;
+  auto more_p = [&] { if (P.todo == 0 && nxt.rows) start_p(nxt); };
+  auto more_q = [&] { if (Q.todo == 0 && nxt.rows) start_q(nxt); };
+  start_p(cur);
+  start_q(cur);
+  pipe.begin(more_p, more_q);
+  for (int round = 1;; ++round) {
     f32x4 acc[PF][QF];
     clear(acc);
-    const int trow = row0, tq = nq, tn0 = n0;
-    const bool idle = tn0 + (PAIR ? wp * PF * 8 : wp * PF * 16) >= N;     // no columns for this wave
-    pipe.run(nk, idle ? 0 : tq - wq * QF * 16, acc, none, none);
-    have = set_up(round);
-    settled();
-    if (have) pipe.begin(none, none);
+    const int trow = cur.row, tq = cur.rows, tn0 = cur.n0;
+    const bool idle = tn0 + wp * (BN / WP) >= N;                    // no columns for this wave
+    const int live = idle ? 0 : tq - wq * QF * 16;
+    constexpr int kStores = 4 * QF;
+    if (live >= QF * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc, more_p, more_q);
+    else pipe.template run<false, kStores>(nk, live, round > 1, acc, more_p, more_q);
 
     // what the results' places are made of is worked out here, not kept during the products
     const int ln = here(lane);
@@ -584,7 +611,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
     const int64_t o0 = (int64_t)trow * ldo + tn0;
     const Window out(a.out + o0), gu(OP == FWD1 ? a.gu_out + 2 * o0 - tn0 : a.gu_in + o0);
     const bool save = OP == FWD1 && a.gu_out;
-    const int c = wp * BN / WP + (ln & 15) * (PAIR ? 2 : 4);
+    const int c = wp * (BN / WP) + (ln & 15) * (PAIR ? 2 : 4);
     const bool in = tn0 + c < N;
 #pragma unroll
     for (int q = 0; q < QF; ++q) {
@@ -625,7 +652,11 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);         // or all results are worked on at once, and spill
     }
+    if (!nxt.rows) break;
+    cur = nxt;
+    nxt = tile(round + 1);
   }
+  settled();                      // LDS is not given up while loads may still write to it
 #endif
 }
 
@@ -662,98 +693,118 @@ __global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
   const int per = p1 * q1 + p2 * q2;
   const int tiles = (s.E + np) * per;
 
-  Tiles pipe(smem, wave, lane);
-  auto& P = pipe.P;
-  auto& Q = pipe.Q;
-  // of the tile that is set up
-  int round = 0, target = 0, p0 = 0, q0 = 0, pcols = 0, qcols = 0, steps = 0;
-  int fp = 0, fq = 0, fend = 0;                 // the fallback pieces that each side has yet to take
-  const char *psrc = nullptr, *qsrc = nullptr;
-  float* out = nullptr;
-
-  auto start = [](auto& side, const char* src, int row, int n) {
-    side.at = src + (int64_t)row * side.ld + side.skip;
-    side.left = n;
+  // A tile: the target's first segment and its fallback pieces [f0, f1), which product, where.
+  struct Tile {
+    int target, row, n, f0, f1, steps, down, p0, q0;        // steps 0: none
+    float* out;
   };
-  // on to the next piece with rows, where a side has done its segment
-  auto walk = [&](auto& side, const char* src, int& f) {
-    while (side.left <= 0 && f < fend) {
-      const Seg fb = load_seg(plan, s, s.E + f, np);
-      ++f;
-      if (uni(fb.w) == target && uni(fb.n) > 0) start(side, src, uni(fb.row0), uni(fb.n));
-      settled();
-    }
-  };
-  auto walk_p = [&] { walk(P, psrc, fp); };
-  auto walk_q = [&] { walk(Q, qsrc, fq); };
-
-  // sets up the workgroup's next tile; false where there is none
-  auto set_up = [&]() -> bool {
-    for (;; ) {
+  int round = 0;
+  auto tile = [&]() -> Tile {
+    for (;;) {
       const int first = tile_of(round, 0, gridDim.x);
       const int t = tile_of(round, blockIdx.x, gridDim.x);
       ++round;
-      if (first >= tiles) return false;
+      if (first >= tiles) return Tile{};
       if (t >= tiles) continue;
-      target = t / per;
-      int local = t - target * per;
-      Seg seg = load_seg(plan, s, target, np);
-      fp = fq = fend = 0;
-      if (target < s.E) {
-        if (!valid) seg.n = 0;
+      Tile r{};
+      r.target = t / per;
+      int local = t - r.target * per;
+      const Seg seg = scalar_seg(plan, s, r.target, np);
+      r.row = seg.row0;
+      r.n = valid ? seg.n : 0;
+      if (r.target < s.E) {
         if (np) {
-          fp = uni(min(max(plan[s.o_pfirst + target], 0), np));
-          fend = fp + uni(min(max(plan[s.o_pnum + target], 0), np - fp));
+          r.f0 = min(max(scalar(plan + s.o_pfirst + r.target), 0), np);
+          r.f1 = r.f0 + min(max(scalar(plan + s.o_pnum + r.target), 0), np - r.f0);
         }
-        out = a.home + target * a.G_el;
+        r.out = a.home + r.target * a.G_el;
       } else {
-        const int w = uni(seg.w);
-        if (uni(seg.n) == 0 || w < s.E) continue;       // a fallback piece: in its home's sum
-        out = a.rep + (w - s.E) * a.G_el;
+        if (seg.n == 0 || seg.w < s.E) continue;         // a fallback piece: in its home's sum
+        r.out = a.rep + (seg.w - s.E) * a.G_el;
       }
-      fq = fp;
-      const bool down = local >= p1 * q1;
-      if (down) local -= p1 * q1;
+      r.down = local >= p1 * q1;
+      if (r.down) local -= p1 * q1;
       int tq, tp;
-      band(local, down ? q2 : q1, down ? p2 : p1, &tq, &tp);
-      p0 = tp * BP;
-      q0 = tq * BQ;
-      pcols = down ? a.I : a.H;
-      qcols = down ? a.H : 2 * a.I;
-      psrc = reinterpret_cast<const char*>(down ? a.h : a.recv);
-      qsrc = reinterpret_cast<const char*>(down ? a.g_y : a.g_gu);
-      if (down) out += 2ll * a.I * a.H;
-      P.ld = pcols * 2;
-      Q.ld = qcols * 2;
-      P.skip = p0 * 2;
-      Q.skip = q0 * 2;
-      P.init_ks(wave, lane, pcols - p0);
-      Q.init_ks(wave, lane, qcols - q0);
-      start(P, psrc, uni(seg.row0), uni(seg.n));
-      start(Q, qsrc, uni(seg.row0), uni(seg.n));
-      steps = (P.left + G::BK - 1) / G::BK;
-      for (int f = fp; f < fend; ++f) {
-        const Seg fb = load_seg(plan, s, s.E + f, np);
-        if (uni(fb.w) == target) steps += (uni(fb.n) + G::BK - 1) / G::BK;
+      band(local, r.down ? q2 : q1, r.down ? p2 : p1, &tq, &tp);
+      r.p0 = tp * BP;
+      r.q0 = tq * BQ;
+      if (r.down) r.out += 2ll * a.I * a.H;
+      r.steps = (r.n + BK - 1) / BK;
+      for (int f = r.f0; f < r.f1; ++f) {
+        const Seg fb = scalar_seg(plan, s, s.E + f, np);
+        if (fb.w == r.target) r.steps += (fb.n + BK - 1) / BK;
       }
-      if (steps == 0 && a.accumulate) continue;
-      return true;
+      if (r.steps == 0 && a.accumulate) continue;
+      r.steps = max(r.steps, G::NB);             // P loads NB steps ahead, into one more tile only
+      return r;
     }
   };
 
-  bool have = set_up();
-  if (have && steps) pipe.begin(walk_p, walk_q);
-  while (have) {
+  Tiles pipe(smem, wave, lane);
+  auto& P = pipe.P;
+  auto& Q = pipe.Q;
+  Tile cur = tile(), nxt = tile();
+  if (!cur.steps) return;
+  int tp = 0, fp = 0, ep = 0, tq = 0, fq = 0, eq = 0;      // each side's target, next piece and last
+  auto start_p = [&](const Tile& t) {
+    P.ld = (t.down ? a.I : a.H) * 2;
+    P.skip = t.p0 * 2;
+    P.at = reinterpret_cast<const char*>(t.down ? a.h : a.recv) + (int64_t)t.row * P.ld + P.skip;
+    P.left = t.n;
+    P.todo = t.steps;
+    P.init_ks(wave, here(lane), (t.down ? a.I : a.H) - t.p0);
+    tp = t.target;
+    fp = t.f0;
+    ep = t.f1;
+  };
+  auto start_q = [&](const Tile& t) {
+    Q.ld = (t.down ? a.H : 2 * a.I) * 2;
+    Q.skip = t.q0 * 2;
+    Q.at = reinterpret_cast<const char*>(t.down ? a.g_y : a.g_gu) + (int64_t)t.row * Q.ld + Q.skip;
+    Q.left = t.n;
+    Q.todo = t.steps;
+    Q.init_ks(wave, here(lane), (t.down ? a.H : 2 * a.I) - t.q0);
+    tq = t.target;
+    fq = t.f0;
+    eq = t.f1;
+  };
+  // on to the next fallback piece with rows, where a side has done its segment
+  auto walk = [&](auto& side, const char* src, int target, int& f, int end) {
+    while (side.left <= 0 && f < end) {
+      const Seg fb = scalar_seg(plan, s, s.E + f, np);
+      ++f;
+      if (fb.w == target && fb.n > 0) {
+        side.at = src + (int64_t)fb.row0 * side.ld + side.skip;
+        side.left = fb.n;
+      }
+    }
+  };
+  bool down_p = false, down_q = false;
+  auto more_p = [&] {
+    if (P.todo == 0 && nxt.steps) {
+      start_p(nxt);
+      down_p = nxt.down;
+    }
+    walk(P, reinterpret_cast<const char*>(down_p ? a.h : a.recv), tp, fp, ep);
+  };
+  auto more_q = [&] {
+    if (Q.todo == 0 && nxt.steps) {
+      start_q(nxt);
+      down_q = nxt.down;
+    }
+    walk(Q, reinterpret_cast<const char*>(down_q ? a.g_y : a.g_gu), tq, fq, eq);
+  };
+  start_p(cur);
+  start_q(cur);
+  down_p = down_q = cur.down;
+  pipe.begin(more_p, more_q);
+  for (bool later = false;; later = true) {
     f32x4 acc[PF][QF];
     clear(acc);
-    const int tp0 = p0, tq0 = q0, tpc = pcols, tqc = qcols;
-    const bool add = a.accumulate && target < s.E;
-    float* const tout = out;
-    if (steps) pipe.run_all(steps, acc, walk_p, walk_q);
-    have = set_up();
-    settled();
-    if (have && steps) pipe.begin(walk_p, walk_q);
-
+    pipe.template run<true, 4 * QF>(cur.steps, 0, later, acc, more_p, more_q);
+    const int tp0 = cur.p0, tq0 = cur.q0, tpc = cur.down ? a.I : a.H, tqc = cur.down ? a.H : 2 * a.I;
+    const bool add = a.accumulate && cur.target < s.E;
+    float* const tout = cur.out;
     const Window o(tout + (int64_t)tq0 * tpc + tp0);
     const int ln = here(lane), c = wp * 64 + (ln & 15) * 4;
     const bool in = tp0 + c < tpc;
@@ -769,13 +820,17 @@ __global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);         // or all results are worked on at once, and spill
     }
+    if (!nxt.steps) break;
+    cur = nxt;
+    nxt = tile();
   }
+  settled();                      // LDS is not given up while loads may still write to it
 #endif
 }
 
-using Large = Geometry<256, 256, 4, 2, 64, 3>;
-using Medium = Geometry<128, 64, 2, 2, 64, 3>;
-using Small = Geometry<128, 32, 2, 2, 64, 4>;
+using Large = Geometry<256, 256, 4, 2, 3>;
+using Medium = Geometry<128, 64, 2, 2, 3>;
+using Small = Geometry<128, 32, 2, 2, 4>;
 
 template <int OP, class G>
 hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
