@@ -107,6 +107,10 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _check(rc):
     if rc != MOONEP_OK:
         raise MoonepError(f"moonep error {rc}: {lib().moonep_strerror(rc).decode()}")
@@ -116,22 +120,33 @@ def _stream(stream, device):
     """The HIP stream handle to enqueue on: `stream`, else the current stream of the
     tensors' device (not of whichever device happens to be current)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        # the handle itself: building a Stream object around it takes longer than some kernels
+        return _raw_stream(device.index)
+    if stream.device != device:
         raise MoonepError(f"stream is on {stream.device}, the tensors on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _dev(t, dtype, name, device=None):
+    """The device address of `t`, checked."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MoonepError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise MoonepError(f"{name} is on {t.device}, the plan on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MoonepError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise MoonepError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _run(f, device, *args):
+    """One call of the library, with `device` the current one while it launches."""
+    if torch.cuda.current_device() == device.index:
+        _check(f(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args))
 
 
 def moonep_query(R, E, K, S, slots) -> Sizes:
@@ -394,7 +409,8 @@ def _rows(t, dtype, name, rows, cols, device, like):
     """`t` checked to be [rows, cols] (its device pointer comes second), allocated next to
     `like` if it is None."""
     if t is None:
-        t = torch.empty(rows, cols, dtype=dtype, device=like.device)
+        t = like.new_empty((rows, cols)) if like.dtype is dtype else \
+            torch.empty(rows, cols, dtype=dtype, device=like.device)
     p = _dev(t, dtype, name, device)
     if t.numel() != rows * cols:
         raise MoonepError(f"{name} must be [{rows}, {cols}]")
@@ -412,7 +428,7 @@ def _slabs(plan, home, slot, el, dtype, names):
     n = plan.sz.R * plan.sz.slots * pitch
     if (slot.numel() if slot is not None else 0) != n:
         raise MoonepError(f"{names[1]} must be [R, slots, {pitch}]")
-    return hp, (_dev(slot, dtype, names[1], D) if n else ctypes.c_void_p(0)), pitch
+    return hp, (_dev(slot, dtype, names[1], D) if n else None), pitch
 
 
 def _act(act):
@@ -435,11 +451,11 @@ def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=Fals
     wp, sp, W_el = _slabs(plan, home_w, slot_w, 3 * I * H, torch.bfloat16, ("home_w", "slot_w"))
     h, hp = _rows(h, torch.bfloat16, "h", n, I, D, recv)
     y, yp = _rows(y, torch.bfloat16, "y", n, H, D, recv)
-    gp = ctypes.c_void_p(0)
+    gp = None
     if save or gu is not None:
         gu, gp = _rows(gu, torch.bfloat16, "gu", n, 2 * I, D, recv)
-    _check(lib().moonep_expert_ffn(ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, W_el, gp, hp,
-                                   yp, _stream(stream, D)))
+    _run(lib().moonep_expert_ffn, D, ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, W_el, gp, hp,
+         yp, _stream(stream, D))
     return y, h, gu
 
 
@@ -456,8 +472,8 @@ def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu
     wp, sp, W_el = _slabs(plan, home_w, slot_w, 3 * I * H, torch.bfloat16, ("home_w", "slot_w"))
     g_gu, ggp = _rows(g_gu, torch.bfloat16, "g_gu", n, 2 * I, D, g_y)
     g_recv, grp = _rows(g_recv, torch.bfloat16, "g_recv", n, H, D, g_y)
-    _check(lib().moonep_expert_ffn_bwd_data(ctypes.byref(plan.desc), yp, gp, H, I, _act(act), wp, sp,
-                                            W_el, ggp, grp, _stream(stream, D)))
+    _run(lib().moonep_expert_ffn_bwd_data, D, ctypes.byref(plan.desc), yp, gp, H, I, _act(act), wp, sp,
+         W_el, ggp, grp, _stream(stream, D))
     return g_recv, g_gu
 
 
@@ -483,8 +499,8 @@ def moonep_expert_ffn_bwd_weight(plan: Plan, recv, g_y, h, g_gu, home_grad=None,
         rep_grad = torch.empty(plan.sz.R, plan.sz.slots, home_grad.shape[-1], dtype=torch.float32,
                                device=recv.device)
     wp, sp, G_el = _slabs(plan, home_grad, rep_grad, 3 * I * H, torch.float32, ("home_grad", "rep_grad"))
-    _check(lib().moonep_expert_ffn_bwd_weight(ctypes.byref(plan.desc), rp, yp, hp, gp, H, I, wp, sp, G_el,
-                                              int(bool(accumulate)), _stream(stream, D)))
+    _run(lib().moonep_expert_ffn_bwd_weight, D, ctypes.byref(plan.desc), rp, yp, hp, gp, H, I, wp, sp, G_el,
+         int(bool(accumulate)), _stream(stream, D))
     return home_grad, rep_grad
 
 
@@ -493,7 +509,7 @@ def _norm_args(x, gamma, res, h, rstd, stats):
     xp = _dev(x, torch.bfloat16, "x")
     D, H = x.device, x.shape[-1]
     T = x.numel() // H if H else 0
-    none = ctypes.c_void_p(0)
+    none = None
     gp = _dev(gamma, torch.bfloat16, "gamma", D)
     if gamma.numel() != H:
         raise MoonepError("gamma must be [H]")
@@ -520,7 +536,7 @@ def moonep_rmsnorm(x, gamma, eps=1e-6, res=None, out=None, h=None, rstd=None, st
     if out is None:
         out = torch.empty_like(x)
     op = _rows(out, torch.bfloat16, "out", T, H, D, x)[1]
-    _check(lib().moonep_rmsnorm(xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D)))
+    _run(lib().moonep_rmsnorm, D, xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D))
     return out, h, rstd
 
 
@@ -534,7 +550,7 @@ def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None
     `rows.view(torch.bfloat16)` is what moonep_dispatch moves.  Returns (rows, h, rstd)."""
     D, T, H, xp, rp, gp, h, hp, rstd, sp = _norm_args(x, gamma, res, h, rstd, stats)
     rows, op = _rows(rows, torch.uint8, "rows", T, moonep_q8_row_bytes(H), D, x)
-    _check(lib().moonep_rmsnorm_q8(xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D)))
+    _run(lib().moonep_rmsnorm_q8, D, xp, rp, gp, eps, T, H, op, hp, sp, _stream(stream, D))
     return rows, h, rstd
 
 
@@ -549,7 +565,7 @@ def moonep_q8_unpack(rows, H, out=None, stream=None):
         raise MoonepError(f"rows must be [N, {rb}] bytes")
     N, D = rows.numel() // rb, rows.device
     out, op = _rows(out, torch.bfloat16, "out", N, H, D, rows)
-    _check(lib().moonep_q8_unpack(rp, N, H, op, _stream(stream, D)))
+    _run(lib().moonep_q8_unpack, D, rp, N, H, op, _stream(stream, D))
     return out
 
 
@@ -565,7 +581,7 @@ def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, 
     sp = _dev(rstd, torch.float32, "rstd", D)
     if gamma.numel() != H or rstd.numel() != T:
         raise MoonepError("gamma must be [H] and rstd [T]")
-    ghp = _rows(g_h, torch.bfloat16, "g_h", T, H, D, g_out)[1] if g_h is not None else ctypes.c_void_p(0)
+    ghp = _rows(g_h, torch.bfloat16, "g_h", T, H, D, g_out)[1] if g_h is not None else None
     g_x, xp = _rows(g_x, torch.bfloat16, "g_x", T, H, D, g_out)
     g_gamma, ggp = _rows(g_gamma, torch.float32, "g_gamma", 1, H, D, g_out)
     need = _bytes(lib().moonep_rmsnorm_bwd_workspace(T, H))
@@ -574,7 +590,7 @@ def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, 
     wp = _dev(workspace, torch.uint8, "workspace", D)
     if workspace.numel() < need:
         raise MoonepError(f"workspace must hold {need} bytes")
-    _check(lib().moonep_rmsnorm_bwd(op, hp, gp, sp, ghp, T, H, wp, xp, ggp, _stream(stream, D)))
+    _run(lib().moonep_rmsnorm_bwd, D, op, hp, gp, sp, ghp, T, H, wp, xp, ggp, _stream(stream, D))
     return g_x, g_gamma.view(H)
 
 
