@@ -828,7 +828,8 @@ __global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
 #endif
 }
 
-using Large = Geometry<256, 256, 4, 2, 3>;
+using Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU, the others two of 4
+using Wide = Geometry<128, 128, 2, 2, 3>;
 using Medium = Geometry<128, 64, 2, 2, 3>;
 using Small = Geometry<128, 32, 2, 2, 4>;
 
@@ -845,12 +846,24 @@ hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Which tile: rows of P are weights, read once for each BQ rows of a group, so BQ goes by the mean
+// of an expert's rows; but large tiles have to be enough for all CUs.  Measured on MI355X, us
+// for the two launches with 64 experts (mean rows: Small, Medium, Wide, Large):
+//   forward,   H 7168, I 2048     16: 1074, 1086, 1093, 1127     32: 1197, 1106, 1112, 1134
+//                                 64: 1657, 1244, 1172, 1169    128: 2662, 1715, 1515, 1256
+//   forward,   H 2048, I 512      32:  110,  126,  133,  149     64:  129,  125,  135,  149
+//                                128:  180,  146,  145,  167    512:  509,  355,  288,  266
+//   gradient,  H 2048, I 1024     64:  254,  222,  252,  260    128:  373,  277,  269,  287
+//                                256:  620,  411,  358,  345    512: 1154,  709,  587,  518
 template <int OP>
 hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
   const int64_t mean = a.s.A / a.s.E;
-  if (mean <= 24) return launch_rows_as<OP, Small>(a, 2, st);
-  if (mean <= 96) return launch_rows_as<OP, Medium>(a, 2, st);
-  return launch_rows_as<OP, Large>(a, 1, st);
+  const int N = OP == FWD1 ? 2 * a.I : OP == BWD1 ? a.I : a.H;
+  auto tiles = [&](int bp, int bq) { return (a.s.E + a.s.A / bq) * ((N + bp - 1) / bp); };
+  if (mean >= 192 || (mean > 48 && tiles(256, 256) >= 4 * kCus)) return launch_rows_as<OP, Large>(a, 1, st);
+  if (mean > 96) return launch_rows_as<OP, Wide>(a, 2, st);
+  if (mean > 48 || (mean > 20 && tiles(128, 64) >= 8 * kCus)) return launch_rows_as<OP, Medium>(a, 2, st);
+  return launch_rows_as<OP, Small>(a, 2, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

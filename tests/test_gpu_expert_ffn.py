@@ -162,6 +162,10 @@ CASES = [
     (4, 8, 2, 700, 2, 320, 456, 1.0),        # hundreds of rows to a group
     (2, 2, 1, 1500, 1, 512, 264, 0.4),       # over a thousand
     (16, 384, 8, 8, 4, 64, 32, 5.0),         # many experts, few rows
+    (2, 6, 2, 180, 1, 136, 200, 1.0),        # around a hundred rows to an expert
+    (8, 64, 4, 64, 2, 256, 1408, 0.8),       # tens of rows, many columns: the gate and up product's
+    (8, 64, 4, 80, 2, 3584, 64, 0.8),        # and the down product's
+    (64, 1024, 2, 32, 256, 8, 8, 6.0),       # as many experts, ranks and slots as there can be
 ]
 
 
@@ -170,6 +174,15 @@ CASES = [
 def test_against_64_bits(R, E, K, S, slots, H, I, mv, act):
     say(f"ffn R={R} E={E} K={K} S={S} slots={slots} H={H} I={I} maxvio={mv} {act}")
     Case(R, E, K, S, slots, H, I, mv, 40 + R + E + S).check(act, 77)
+
+
+def test_more_tiles_than_a_look_up_holds():
+    """Over 64 tiles to each workgroup: 256 experts and rows of 32768."""
+    say("ffn many tiles")
+    c = Case(2, 256, 2, 128, 2, 32768, 8, 0.5, 71)
+    y, h, gu = c.check_forward("silu")
+    c.check_rows_gradient("silu", gu, 72)
+    torch.cuda.synchronize()
 
 
 @pytest.mark.parametrize("slots", [0, 2])
