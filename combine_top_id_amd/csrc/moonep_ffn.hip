@@ -508,9 +508,11 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   // Lane l sums the row tiles of segments [l * per, l * per + per).
   const int per = (nseg + 63) / 64;
   int sum = 0;
+  Seg mine{0, 0, 0};                           // the lane's last
   for (int j = 0; j < per; ++j) {
     const int i = lane * per + j;
-    if (i < nseg) sum += (load_seg(plan, a.s, i, np).n + BQ - 1) / BQ;
+    if (i < nseg) mine = load_seg(plan, a.s, i, np);
+    if (i < nseg) sum += (mine.n + BQ - 1) / BQ;
   }
   sum = wave_sums(sum, lane);
   const int tiles = min(__builtin_amdgcn_readlane(sum, 63), a.tiles_bound) * nt;
@@ -519,7 +521,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   // no barrier, and 64 rounds without a wait for memory.
   int lane_row = -1;                            // first row, or none
   uint32_t lane_rest = 0;                       // rows - 1, column tile, weight
-  auto look_up = [&](int first) {
+  auto look_up = [&](int first, bool held) {
     const int t = tile_of(first + lane, blockIdx.x, gridDim.x);
     const int want = t < 0 || t >= tiles ? 0 : t / nt;
     int l = 0;                                  // the sums that are at most `want`
@@ -530,11 +532,16 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
     below = l ? below : 0;
     Seg g{0, 0, 0};
     int mt = 0;
-    for (int j = 0; j < per; ++j) {
-      g = load_seg(plan, a.s, min(l * per + j, nseg - 1), np);
+    if (held && per == 1) {                     // the other lanes hold them all: no second read
+      g = Seg{__shfl(mine.row0, l), __shfl(mine.n, l), __shfl(mine.w, l)};
       mt = (g.n + BQ - 1) / BQ;
-      if (below + mt > want) break;
-      below += mt;
+    } else {
+      for (int j = 0; j < per; ++j) {
+        g = load_seg(plan, a.s, min(l * per + j, nseg - 1), np);
+        mt = (g.n + BQ - 1) / BQ;
+        if (below + mt > want) break;
+        below += mt;
+      }
     }
     lane_row = -1;
     const int local = t - below * nt;
@@ -550,13 +557,13 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
     int row, rows, n0, w;                       // rows 0: none
   };
   auto tile = [&](int round) -> Tile {
-    if (round && (round & 63) == 0) look_up(round);
+    if (round && (round & 63) == 0) look_up(round, false);
     const int row = __builtin_amdgcn_readlane(lane_row, round & 63);
     const uint32_t rest = __builtin_amdgcn_readlane(lane_rest, round & 63);
     if (row < 0) return {0, 0, 0, 0};
     return {row, (int)(rest & 255) + 1, (int)(rest >> 8 & 511) * BN, (int)(rest >> 17)};
   };
-  look_up(0);
+  look_up(0, true);
 
   Tiles pipe(smem, wave, lane);
   auto& P = pipe.P;
