@@ -298,13 +298,14 @@ void shape(int nvec, int* threads, int* u) {
   }
 }
 
-// Workgroups of the backward kernel: one for each CU, or as many short ones as take its place.
+// Workgroups of the backward kernel: one for each CU, or as many short ones as take its place
+// if they have four rows each (each costs a row of partial sums).
 // At 16384 rows of 7168 (940 MB) one measured 152 us (6.2 TB/s) with the column sums, two 162,
 // three without the rows ahead 190.
 int bwd_blocks(int64_t T, int H) {
   int threads, u;
   shape(H / 8, &threads, &u);
-  return (int)std::min<int64_t>(T, kCus * std::max(1, kThreads / threads));
+  return (int)std::min<int64_t>(T, std::max<int64_t>(kCus, std::min<int64_t>(kCus * (kThreads / threads), T / 4)));
 }
 
 // A launch has fewer than 2^32 threads.
