@@ -906,6 +906,8 @@ int check_ffn(const moonep_plan_desc* d, int H, int I) {
   if (rc != MOONEP_OK) return rc;
   if (H <= 0 || H % 8 != 0 || I <= 0 || I % 8 != 0) return MOONEP_EINVAL;
   if (H > MOONEP_MAX_FFN || I > MOONEP_MAX_FFN) return MOONEP_ELIMIT;
+  // an expert's up rows are addressed from its gate rows, with a tile to spare, in 31 bits
+  if ((int64_t)(I + 256) * H * 2 > INT32_MAX) return MOONEP_ELIMIT;
   // tiles are counted in 32 bits, for the smallest tile
   const int64_t mt = d->sz.A / 32 + d->sz.E + d->sz.P_max;
   if (mt * ((std::max(H, I) + 63) / 64) > INT32_MAX) return MOONEP_ELIMIT;

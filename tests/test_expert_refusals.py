@@ -64,6 +64,7 @@ def test_experts_refuse(lib, desc, call, ptrs):
         assert call(lib, desc, **bad) == EINVAL, bad
     assert call(lib, desc, H=32776) == ELIMIT
     assert call(lib, desc, I=32776) == ELIMIT
+    assert call(lib, desc, H=32768, I=32768) == ELIMIT      # an expert's matrix beyond 31 bits of bytes
     pitch = "G_el" if call is weight else "W_el"
     assert call(lib, desc, **{pitch: 3 * 64 * 32 - 8}) == EINVAL
     assert call(lib, desc, **{pitch: 3 * 64 * 32 + 2}) == EINVAL
@@ -80,9 +81,9 @@ def test_forward_refuses_a_misaligned_save_buffer(lib, desc):
 
 
 def test_more_tiles_than_32_bits(lib, desc):
-    # a plan of 2^27 assignments and matrices of 32768 columns
+    # a plan of 2^30 assignments and rows of 32768 columns
     desc.sz = M.moonep_query(64, 64, 1, 1 << 24, 0)
-    assert ffn(lib, desc, H=32768, I=32768, slot=None) == ELIMIT
+    assert ffn(lib, desc, H=32768, I=64, slot=None) == ELIMIT
 
 
 def test_norm_refuses(lib):
