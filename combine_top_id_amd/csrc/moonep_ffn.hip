@@ -21,8 +21,6 @@ namespace moonep {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -31,7 +29,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define LDS __attribute__((address_space(3)))
 
-constexpr int kMaxSegs = 2 * MOONEP_MAX_E + MOONEP_MAX_R;
 constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: reads as zero
 constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
 constexpr int kCus = 256;
@@ -115,12 +112,13 @@ __device__ __forceinline__ Seg scalar_seg(const int32_t* plan, const moonep_size
 // for the builtin the compiler waits for every such load before any LDS read that it cannot
 // tell apart from it, which here is each one, and the next steps' loads would never be in
 // flight during this step's products.  No register is written, so there is none to wait
-// for; arrive() is the wait.  (m0 holds the LDS address; gfx9 wants one instruction
-// between writing it and the load.)
+// for; arrive() is the wait.  m0 holds the LDS address.  gfx9 wants one instruction between
+// writing it and the load, and five between a lane's value read into a scalar register,
+// as which the compiler may bring back a spilled one, and a load that takes it.
 template <int OFF>
 __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(to), "v"(voff), "s"(rsrc), "i"(OFF) : "memory", "scc");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(to), "v"(voff), "s"(rsrc), "i"(OFF) : "memory", "scc", "m0");
 }
 
 // ---------------------------------------------------------------------------------------
@@ -409,7 +407,7 @@ __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xF
 // act(z), and its slope.  SiLU: z s with s = 1 / (1 + e^-z), slope s + z s (1 - s).
 // GELU in its tanh form: z p with p = (1 + tanh(u)) / 2 = 1 / (1 + e^-2u),
 // u = c (z + 0.044715 z^3), slope p + 2 z p (1 - p) u'.  Beyond |z| = 16 p is exactly 0 or
-// 1 in fp32 and u' would overflow, so u is taken of z cut to that range.
+// 1 in fp32 and u' would overflow, so u is taken of z cut to that range (a NaN stays one).
 __device__ __forceinline__ float act_of(float z, int act, float* slope) {
   if (act == MOONEP_ACT_SILU) {
     const float s = 1.f / (1.f + __expf(-z));
@@ -417,7 +415,7 @@ __device__ __forceinline__ float act_of(float z, int act, float* slope) {
     return z * s;
   }
   const float c = 0.7978845608028654f;
-  const float zc = fminf(fmaxf(z, -16.f), 16.f);
+  const float zc = z < -16.f ? -16.f : z > 16.f ? 16.f : z;
   const float z2 = zc * zc;
   const float p = 1.f / (1.f + __expf(-2.f * c * (zc + 0.044715f * zc * z2)));
   *slope = p + 2.f * zc * p * (1.f - p) * c * (1.f + 0.134145f * z2);

@@ -421,10 +421,10 @@ def _slabs(plan, home, slot, el, dtype, names):
     """Device pointers and the pitch of an [E, pitch] and an [R, slots, pitch] array of
     experts' slabs of at least `el` elements."""
     D = plan.blob.device
+    hp = _dev(home, dtype, names[0], D)
     pitch = home.shape[-1]
     if home.numel() != plan.sz.E * pitch or pitch < el:
         raise MoonepError(f"{names[0]} must be [E, 3*I*H or more]")
-    hp = _dev(home, dtype, names[0], D)
     n = plan.sz.R * plan.sz.slots * pitch
     if (slot.numel() if slot is not None else 0) != n:
         raise MoonepError(f"{names[1]} must be [R, slots, {pitch}]")

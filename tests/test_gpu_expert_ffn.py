@@ -219,6 +219,29 @@ def test_large_and_nonfinite_gates():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_nonfinite_rows_of_the_gradient(act):
+    """A NaN gate, a NaN up and a NaN in g_y reach their row's gradients and no other row."""
+    say(f"ffn nonfinite gradients {act}")
+    c = Case(2, 4, 2, 100, 2, 64, 48, 1.0, 24)
+    I = c.I
+    _, _, gu = M.moonep_expert_ffn(c.plan, c.recv, c.home_w, c.slot_w, I, act=act, save=True)
+    g_y = c.rows_of(c.H, 25)
+    clean, g_clean = M.moonep_expert_ffn_bwd_data(c.plan, g_y, gu, c.home_w, c.slot_w, I, act=act)
+    live = torch.nonzero(c.mapped).flatten()
+    gate, up, grad = (int(live[k]) for k in (5, 90, 140))
+    gu[gate, 3], gu[up, I + 4], g_y[grad, 7] = NAN, NAN, NAN
+    g_recv, g_gu = M.moonep_expert_ffn_bwd_data(c.plan, g_y, gu, c.home_w, c.slot_w, I, act=act)
+    bad = torch.isnan(g_gu)
+    assert bad[gate].nonzero().flatten().tolist() == [3, I + 3]
+    assert bad[up].nonzero().flatten().tolist() == [4]
+    assert bad[grad].all() and torch.isnan(g_recv[[gate, up, grad]]).all()
+    rest = c.mapped.clone()
+    rest[[gate, up, grad]] = False
+    assert torch.equal(g_recv[rest], clean[rest]) and torch.equal(g_gu[rest], g_clean[rest])
+    torch.cuda.synchronize()
+
+
 def test_gradients_against_differences():
     """The library's gradients along random directions against central differences of the
     64-bit forward pass.  bf16 rounding of g_gate and g_up (2^-8 each, independent over
@@ -356,6 +379,37 @@ def test_two_calls_at_once():
     for k, c in enumerate(cs):
         for o in outs[k]:
             assert torch.equal(o[c.mapped], alone[k][c.mapped])
+
+
+def test_stream_argument():
+    """Calls given a stream run on it, in order, whatever the current stream is."""
+    say("ffn stream argument")
+    c = Case(4, 16, 2, 200, 4, 256, 128, 2.0, 53)
+    g_y = c.rows_of(c.H, 54)
+
+    def step(stream):
+        y, h, gu = M.moonep_expert_ffn(c.plan, c.recv, c.home_w, c.slot_w, c.I, stream=stream, h=b[0], gu=b[1], y=b[2])
+        g_recv, g_gu = M.moonep_expert_ffn_bwd_data(c.plan, g_y, gu, c.home_w, c.slot_w, c.I, stream=stream,
+                                                    g_gu=b[3], g_recv=b[4])
+        home, rep = M.moonep_expert_ffn_bwd_weight(c.plan, c.recv, g_y, h, g_gu, stream=stream, home_grad=b[5],
+                                                   rep_grad=b[6])
+        return y[c.mapped], g_recv[c.mapped], home
+
+    def buffers():
+        el = 3 * c.H * c.I
+        return [c.empty(c.I), c.empty(2 * c.I), c.empty(c.H), c.empty(2 * c.I), c.empty(c.H),
+                torch.empty(c.E, el, device="cuda"), torch.empty(c.R, c.slots, el, device="cuda")]
+
+    b = buffers()
+    want = step(None)
+    b = buffers()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step(s)
+    s.synchronize()
+    for a, w in zip((b[2][c.mapped], b[4][c.mapped], b[5]), want):
+        assert torch.equal(a, w)
+    torch.cuda.synchronize()
 
 
 def test_block_trains_as_without_replication():
