@@ -13,6 +13,7 @@
 // neighbours, and those of lanes that follow each other are too.  A CU writes such runs
 // four times as fast as 16-byte pieces of as many rows as it has lanes (141 and 35 GB/s),
 // and all of an output is written at a tile's end.
+#include <cmath>
 #include <type_traits>
 
 #include "moonep_internal.h"
@@ -859,9 +860,9 @@ __global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
 #endif
 }
 
-using Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU, the others two of 4
-using Wide = Geometry<128, 128, 2, 2, 3>;
-using Medium = Geometry<128, 64, 2, 2, 3>;
+using Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU
+using Tall = Geometry<256, 128, 4, 2, 3>;
+using Medium = Geometry<128, 64, 2, 2, 3>;       // two of 4
 using Small = Geometry<128, 32, 2, 2, 4>;
 
 template <int OP, class G>
@@ -877,23 +878,42 @@ hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which tile: rows of P are weights, read once for each BQ rows of a group, so BQ goes by the mean
-// of an expert's rows; but large tiles have to be enough for all CUs.  Measured on MI355X, us
-// for the two launches with 64 experts (mean rows: Small, Medium, Wide, Large):
-//   forward,   H 7168, I 2048     16: 1074, 1086, 1093, 1127     32: 1197, 1106, 1112, 1134
-//                                 64: 1657, 1244, 1172, 1169    128: 2662, 1715, 1515, 1256
-//   forward,   H 2048, I 512      32:  110,  126,  133,  149     64:  129,  125,  135,  149
-//                                128:  180,  146,  145,  167    512:  509,  355,  288,  266
-//   gradient,  H 2048, I 1024     64:  254,  222,  252,  260    128:  373,  277,  269,  287
-//                                256:  620,  411,  358,  345    512: 1154,  709,  587,  518
+// Which tile.  The large ones read the weights and the rows fewer times and multiply at the best
+// rate, but fill up more rows with zeros and leave CUs without a tile.  So each launch takes
+// the tile whose time is the least by a model: rounds of tiles over the CUs times a tile's
+// time, which is its steps and about four more for its start and end.  Below the weights' own
+// time at 6 TB/s, tiles differ only in what they leave of it, about a quarter of theirs.
+// An expert's group and its replicas end inside a tile: half of one to each group.
+// Measured on MI355X, us for the two launches (Large, Tall, Medium, Small; mean rows of an
+// expert), of which the model takes the best or one within 4%, but for the last two (7%, 14%):
+//   64 experts, forward,  H 7168, I 2048    16: 1129, 1093, 1084, 1072    64: 1153, 1130, 1238, 1662
+//                                          128: 1259, 1292, 1702, 2663   256: 1832, 1800, 2739, 4987
+//   64 experts, gradient, H 2048, I 1024    32:  251,  220,  225,  208    64:  259,  232,  220,  255
+//                                          128:  277,  251,  275,  372   512:  517,  529,  700, 1147
+//   16 experts, forward,  H 2048, I 1024   128:   86,   71,   96,  111   256:   93,  108,  123,  156
+//    4 experts, forward,  H 2048, I 512    128:   52,   44,   28,   26   256:   67,   43,   29,   34
+//   32 experts, gradient, H 1000, I 680   256:  100,   93,  115,  157
+//    4 experts, gradient, H 1024, I 512  1024:   72,   46,   41,   45
+// (128x128 tiles, two workgroups to a CU, were never more than 3% before the best of these.)
 template <int OP>
 hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
-  const int64_t mean = a.s.A / a.s.E;
   const int N = OP == FWD1 ? 2 * a.I : OP == BWD1 ? a.I : a.H;
-  auto tiles = [&](int bp, int bq) { return (a.s.E + a.s.A / bq) * ((N + bp - 1) / bp); };
-  if (mean >= 192 || (mean > 48 && tiles(256, 256) >= 4 * kCus)) return launch_rows_as<OP, Large>(a, 1, st);
-  if (mean > 96) return launch_rows_as<OP, Wide>(a, 2, st);
-  if (mean > 48 || (mean > 20 && tiles(128, 64) >= 8 * kCus)) return launch_rows_as<OP, Medium>(a, 2, st);
+  const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
+  const double groups = (double)std::min<int64_t>(a.s.E + a.s.R - 1, a.s.A);
+  const double weights_us = groups * N * K * 2 / 6e6;
+  // us of a step where a workgroup has its CU alone, and where the CU, or the chip, is full
+  auto us = [&](int bp, int bq, int wgs, double alone, double full) {
+    const double tiles = std::max(groups, (double)a.s.A / bq + groups / 2) * ((N + bp - 1) / bp);
+    const double r = tiles / wgs, rounds = r <= 1 ? 1 : r < 4 ? std::ceil(r) : r + 0.5;
+    const double t = rounds * ((K + BK - 1) / BK + 4.3) * (tiles <= kCus ? alone : full);
+    return std::max(t, weights_us) + 0.24 * t;
+  };
+  const double large = us(256, 256, kCus, 1.22, 1.31), tall = us(256, 128, kCus, 0.71, 0.81);
+  const double medium = us(128, 64, 2 * kCus, 0.43, 0.62), small = us(128, 32, 2 * kCus, 0.37, 0.48);
+  const double least = std::min(std::min(large, tall), std::min(medium, small));
+  if (large == least) return launch_rows_as<OP, Large>(a, 1, st);
+  if (tall == least) return launch_rows_as<OP, Tall>(a, 1, st);
+  if (medium == least) return launch_rows_as<OP, Medium>(a, 2, st);
   return launch_rows_as<OP, Small>(a, 2, st);
 }
 
