@@ -130,10 +130,10 @@ __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to)
 //       of chunk c ^ (r & 7): the 16 lanes that read at once hit different banks.
 //   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, read
 //       transposed.  A fragment of Q is 16 neighbours, and 32-byte unit u of row k is in the
-//       place of u ^ (k & 3 | (k >> 3 & 1) << 2).  A fragment f of P is every fourth run of
-//       four: runs f, f + 4, f + 8 and f + 12 of 64 elements; 16-byte chunk c is in the
-//       place of c ^ (k & 1 | (k & 2) << 2): two lanes to a bank, the best that can be where
-//       only half of each 16 bytes is read.
+//       place of u ^ (k & 3 | (k >> 3 & 1) << 2), or of u ^ (k & 3) where R is 64.  A
+//       fragment f of P is every fourth run of four: runs f, f + 4, f + 8 and f + 12 of 64
+//       elements; 16-byte chunk c is in the place of c ^ (k & 1 | (k & 2) << 2): two lanes
+//       to a bank, the best that can be where only half of each 16 bytes is read.
 // Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
 // global address, since a wave's load fills 1024 consecutive LDS bytes.
 
@@ -141,7 +141,8 @@ template <int R, bool KS, int NW, bool ISP>
 struct Operand {
   static constexpr int kBytes = R * BK * 2;
   static constexpr int kLoads = kBytes / 1024 / NW;
-  static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes);
+  static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes && (!KS || R >= (ISP ? 128 : 64)));
+  static constexpr int kUnit4 = R >= 128;    // KS: a row of 64 has four units only
   uint32_t voff[kLoads];
   int kc;                        // KC: this lane's first k inside a step
   // the next step to load: its address, the k left from there, and the steps of this tile
@@ -166,7 +167,7 @@ struct Operand {
     for (int i = 0; i < kLoads; ++i) {
       const int b = (i * NW + wave) * 1024 + lane * 16;
       const int k = b / (R * 2), cp = b % (R * 2) / 16;
-      const int c = cp ^ (ISP ? (k & 1) | (k & 2) << 2 : ((k & 3) | (k >> 3 & 1) << 2) << 1);
+      const int c = cp ^ (ISP ? (k & 1) | (k & 2) << 2 : ((k & 3) | (k >> 3 & kUnit4) << 2) << 1);
       voff[i] = c * 8 < ncols ? k * ld + c * 16 : kOob;
     }
   }
@@ -206,7 +207,7 @@ __device__ __forceinline__ int fragment_lane(int row0, int lane) {
   if constexpr (!KS) return (row0 + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
   const int g = lane >> 4, j = (lane & 15) >> 2, k = (g * 8 + j) * (R * 2);
   if constexpr (ISP) return k + (((row0 / 8 + (lane & 3) * 2) ^ ((j & 1) | (j & 2) << 2)) << 4);
-  return k + (((row0 / 16) ^ j ^ ((g & 1) << 2)) << 5) + (lane & 3) * 8;
+  return k + (((row0 / 16) ^ j ^ (R >= 128 ? (g & 1) << 2 : 0)) << 5) + (lane & 3) * 8;
 }
 template <int R, bool KS, bool ISP>
 __device__ __forceinline__ bf16x8 fragment(int at, int f, int kk) {
@@ -483,6 +484,13 @@ __device__ __forceinline__ int wave_sums(int v, int lane) {
   return v;
 }
 
+// What bounds it, on MI355X: with hundreds of rows to an expert, power.  512 rows to each of
+// 32 experts, H 7168, I 2048: 1.67 and 0.80 ms, 1170 TF of the formula's products, 1360 with
+// the rows that fill up the groups' last tiles; the matrix units are busy 62% of the time at
+// 1.7 GHz, where few rows run at 2.4 GHz.  (A 16384 x 8192 x 7168 library product: 88% at
+// 1.48 GHz, 1360 TF.)  With few rows, the weights' stream: 64 rows in 64 experts at one
+// token a rank, 4.0 GB of weights in 428 and 227 us, 6.05 TB/s.  The gradient g_gate, g_up
+// with its four more arrays is between the two: 0.41 ms for 49152 rows, H 2048, I 1408.
 template <int OP, class G>
 __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
@@ -706,6 +714,9 @@ struct GradArgs {
   int64_t G_el;
 };
 
+// What bounds it, on MI355X: power again, more of which goes into writing.  16384 rows of 16
+// experts, H 7168, I 2048: 1.55 ms, 930 TF, 4.1 GB; the matrix units busy 50% at 1.6 GHz.
+// Few rows: the writes; 21 experts of 73 rows, H 1000, I 680: 200 MB in 49 us.
 // NT: gradients that the last-level cache cannot hold pass it by: 3-6% faster from 0.8 GB on, 10%
 // slower at 0.2 GB.
 template <class G, bool NT>
@@ -862,7 +873,8 @@ __global__ __launch_bounds__(64 * G::NW, 2) void grad_kernel(const GradArgs a) {
 
 using Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU
 using Tall = Geometry<256, 128, 4, 2, 3>;
-using Medium = Geometry<128, 64, 2, 2, 3>;       // two of 4
+using Square = Geometry<128, 128, 2, 2, 3>;      // two of 4, as the next
+using Medium = Geometry<128, 64, 2, 2, 3>;
 using Small = Geometry<128, 32, 2, 2, 4>;
 
 template <int OP, class G>
@@ -915,6 +927,26 @@ hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
   if (tall == least) return launch_rows_as<OP, Tall>(a, 1, st);
   if (medium == least) return launch_rows_as<OP, Medium>(a, 2, st);
   return launch_rows_as<OP, Small>(a, 2, st);
+}
+
+template <class G, bool NT>
+hipError_t launch_grad_as(const GradArgs& a, int per_cu, hipStream_t st) {
+  hipLaunchKernelGGL((grad_kernel<G, NT>), dim3(per_cu * kCus), dim3(64 * G::NW), 0, st, a);
+  return hipGetLastError();
+}
+
+// Which tile: the largest that still gives the CUs work.  Measured on MI355X, us, by 256x256
+// tiles of the targets (256x256, 128x128, 128x64, the latter two with two workgroups to a CU):
+//    36: 51.7, 38.1, 30.1     66: 55.6, 37.4, 29.4     84: 23.2, 17.2, 16.9    144: 103.6, 64.2, 83.7
+//   142: 18.4, 12.9, 14.7    228: 26.5, 28.6, 33.8    336: 44.3, 44.9, 50.6    912: 57.9, 62.7, 76.7
+hipError_t launch_grad(const GradArgs& a, hipStream_t st) {
+  auto of = [](int64_t n) { return (n + 255) / 256; };
+  const int64_t targets = a.s.E + std::min<int64_t>(a.s.R - 1, (int64_t)a.s.R * a.s.slots);
+  const int64_t tiles = targets * (of(a.H) * of(2 * a.I) + of(a.I) * of(a.H));
+  if (tiles <= kCus / 3) return launch_grad_as<Medium, false>(a, 2, st);
+  if (tiles <= kCus * 5 / 8) return launch_grad_as<Square, false>(a, 2, st);
+  if ((int64_t)a.s.E * 12 * a.I * a.H > kLastLevelCacheBytes) return launch_grad_as<Large, true>(a, 1, st);
+  return launch_grad_as<Large, false>(a, 1, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -1007,10 +1039,7 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
   a.recv = recv; a.g_y = g_y; a.h = h; a.g_gu = g_gu;
   a.home = home_grad; a.rep = rep_grad; a.G_el = G_el;
   (void)hipGetLastError();
-  const bool nt = (int64_t)a.s.E * 12 * I * H > kLastLevelCacheBytes;
-  if (nt) hipLaunchKernelGGL((grad_kernel<Large, true>), dim3(kCus), dim3(64 * Large::NW), 0, stream, a);
-  else hipLaunchKernelGGL((grad_kernel<Large, false>), dim3(kCus), dim3(64 * Large::NW), 0, stream, a);
-  return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
+  return launch_grad(a, stream) == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
 }  // extern "C"
