@@ -279,8 +279,8 @@ int moonep_expert_stub(const moonep_plan_desc* plan, const int32_t* topk_ids,
  *   y       device bf16 [R*NvS, H]
  * H and I are multiples of 8, at most MOONEP_MAX_FFN, with (I + 256) * H < 2^30; W_el is a
  * multiple of 8; all pointers 16-byte aligned.  Padding rows of recv are not read and those
- * of gu, h and y not written.  No output may overlap an input or another output.  EHIP can follow the first of the two
- * launches.  Deterministic. */
+ * of gu, h and y not written.  No output may overlap an input or another output.  EHIP can
+ * follow the first of the two launches.  Deterministic. */
 int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H, int I, int act,
                       const uint16_t* home_w, const uint16_t* slot_w, int64_t W_el, uint16_t* gu,
                       uint16_t* h, uint16_t* y, hipStream_t stream);
