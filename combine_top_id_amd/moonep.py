@@ -6,6 +6,7 @@ fallback: if the library is not built, or no GPU is present, calls raise.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -405,6 +406,18 @@ def _bytes(n):
     return n
 
 
+def _on_its_stream(f):
+    """f, allocating what it is not given on the stream that it is told to use: memory of
+    another stream could be handed on there (a workspace at once) while the call still runs."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kwargs)
+    return call
+
+
 def _rows(t, dtype, name, rows, cols, device, like):
     """`t` checked to be [rows, cols] (its device pointer comes second), allocated next to
     `like` if it is None."""
@@ -437,6 +450,7 @@ def _act(act):
     return ACTIVATIONS[act]
 
 
+@_on_its_stream
 def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=False, h=None, gu=None,
                       y=None, stream=None):
     """The gated feed-forward experts: y[row] = Wd (act(Wg x) * (Wu x)) with x = recv[row] and
@@ -459,6 +473,7 @@ def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=Fals
     return y, h, gu
 
 
+@_on_its_stream
 def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu", g_gu=None,
                                g_recv=None, stream=None):
     """Gradient of moonep_expert_ffn with respect to the rows, from g_y bf16 [R*NvS, H] and the
@@ -477,6 +492,7 @@ def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu
     return g_recv, g_gu
 
 
+@_on_its_stream
 def moonep_expert_ffn_bwd_weight(plan: Plan, recv, g_y, h, g_gu, home_grad=None, rep_grad=None,
                                  accumulate=False, stream=None):
     """Gradient of moonep_expert_ffn with respect to the weights: home_grad fp32 [E, G_el]
@@ -528,6 +544,7 @@ def _norm_args(x, gamma, res, h, rstd, stats):
     return D, T, H, xp, rp, gp, h, hp, rstd, sp
 
 
+@_on_its_stream
 def moonep_rmsnorm(x, gamma, eps=1e-6, res=None, out=None, h=None, rstd=None, stats=True, stream=None):
     """h = bf16(x + res), out = bf16(h * rstd * gamma), rstd = 1 / sqrt(mean(h^2) + eps), row by
     row.  x, res bf16 [T, H], gamma bf16 [H].  Returns (out, h, rstd): h is x where there is
@@ -545,6 +562,7 @@ def moonep_q8_row_bytes(H):
     return _bytes(lib().moonep_q8_row_bytes(H))
 
 
+@_on_its_stream
 def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None, stats=True, stream=None):
     """moonep_rmsnorm with its output as 8-bit rows, uint8 [T, moonep_q8_row_bytes(H)].
     `rows.view(torch.bfloat16)` is what moonep_dispatch moves.  Returns (rows, h, rstd)."""
@@ -554,6 +572,7 @@ def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None
     return rows, h, rstd
 
 
+@_on_its_stream
 def moonep_q8_unpack(rows, H, out=None, stream=None):
     """8-bit rows (uint8 [N, moonep_q8_row_bytes(H)], or the same bytes as bf16 elements, as the
     dispatch returns them) expanded to bf16 [N, H]."""
@@ -569,6 +588,7 @@ def moonep_q8_unpack(rows, H, out=None, stream=None):
     return out
 
 
+@_on_its_stream
 def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, workspace=None, stream=None):
     """Backward of the norm from the stored h bf16 [T, H] and rstd fp32 [T]; g_h, if given, is
     the gradient that reaches h past the norm.  Returns (g_x bf16 [T, H], the gradient of x

@@ -412,6 +412,74 @@ def test_stream_argument():
     torch.cuda.synchronize()
 
 
+def test_allocations_follow_the_stream():
+    """What a call allocates belongs to the stream that it runs on: memory of the current
+    stream could be handed to that one's next work while the call still uses it."""
+    say("ffn allocations")
+    c = Case(4, 16, 2, 64, 4, 128, 64, 2.0, 55)
+    g_y = c.rows_of(c.H, 56)
+    gamma = torch.ones(c.H, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    seen = []
+    empty = torch.empty
+
+    def watched(*shape, **kw):
+        seen.append(torch.cuda.current_stream())
+        return empty(*shape, **kw)
+
+    torch.empty = watched
+    try:
+        y, h, gu = M.moonep_expert_ffn(c.plan, c.recv, c.home_w, c.slot_w, c.I, save=True, stream=s)
+        g_recv, g_gu = M.moonep_expert_ffn_bwd_data(c.plan, g_y, gu, c.home_w, c.slot_w, c.I, stream=s)
+        home, rep = M.moonep_expert_ffn_bwd_weight(c.plan, c.recv, g_y, h, g_gu, stream=s)
+        out, _, rstd = M.moonep_rmsnorm(y, gamma, stream=s)
+        rows, _, _ = M.moonep_rmsnorm_q8(y, gamma, stream=s)
+        back = M.moonep_q8_unpack(rows, c.H, stream=s)
+        g_x, g_gamma = M.moonep_rmsnorm_bwd(out, y, gamma, rstd, stream=s)
+    finally:
+        torch.empty = empty
+    s.synchronize()
+    assert seen and all(x == s for x in seen)
+    held = [(b["address"], b["total_size"], b["stream"]) for b in torch.cuda.memory_snapshot()]
+    for t in (y, h, gu, g_recv, g_gu, home, rep, out, rstd, rows, back, g_x, g_gamma):
+        of = [st for a, n, st in held if a <= t.data_ptr() < a + n]
+        assert of == [s.cuda_stream]
+
+
+def test_rows_past_32_bits():
+    """A buffer of more than 2^31 elements: the last rows of the last group, and all gradients of
+    one expert's weights against those rows' alone."""
+    say("ffn large buffer")
+    R, E, K, S, H, I = 2, 2, 2, 76000, 7168, 8
+    ids = np.tile(np.arange(2, dtype=np.int32), (R * S, 1))
+    c = Case(R, E, K, S, 0, H, I, 0, 57, ids=ids)
+    assert c.rows * H > 2 ** 31
+    y, h, gu = M.moonep_expert_ffn(c.plan, c.recv, c.home_w, None, I, save=True)
+    r0, n, _, e = max(c.groups)
+    s = slice(r0 + n - 70, r0 + n)
+    w = c.home_w[e]
+    _, _, hh, _, _, dh = X.gate_up(c.recv[s], w, H, I, "silu")
+    X.close(h[s], hh, dh, X.UB16, "h")
+    ref, d = X.down(h[s], w, H, I)
+    X.close(y[s], ref, d, X.UB16, "y")
+    # only those rows have an output gradient
+    g_y = torch.zeros_like(c.recv)
+    g_y[s] = bf16(70, H, seed=58)
+    g_recv, g_gu = M.moonep_expert_ffn_bwd_data(c.plan, g_y, gu, c.home_w, None, I)
+    gg, gv, dg, dv = X.back_gu(g_y[s], gu[s], w, H, I, "silu")
+    X.close(g_gu[s], torch.cat([gg, gv], 1), torch.cat([dg, dv], 1), X.UB16, "g_gu")
+    ref, d = X.back_rows(g_gu[s], w, H, I)
+    X.close(g_recv[s], ref, d, X.UB16, "g_recv")
+    home, _ = M.moonep_expert_ffn_bwd_weight(c.plan, c.recv, g_y, h, g_gu)
+    x, gy, hd, ggu = (t[s].double() for t in (c.recv, g_y, h, g_gu))
+    ref = torch.cat([(ggu.T @ x).reshape(-1), (gy.T @ hd).reshape(-1)])
+    mag = torch.cat([(ggu.T.abs() @ x.abs()).reshape(-1), (gy.T.abs() @ hd.abs()).reshape(-1)])
+    X.close(home[e], ref, 70 * X.U32 * mag + 1e-30, X.U32, "weights' gradient")
+    assert (home[1 - e] == 0).all()
+    torch.cuda.synchronize()
+
+
 def test_block_trains_as_without_replication():
     """norm -> 8-bit rows -> dispatch -> expand -> experts -> combine, and its backward pass,
     against each token's experts applied without any plan, in 64 bits."""

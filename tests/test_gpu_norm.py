@@ -237,3 +237,32 @@ def test_capture_and_another_stream():
         torch.cuda.synchronize()
         for n in got:
             assert torch.equal(got[n], o[n]), n
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements: the last rows, as the same rows give alone, and gradients of
+    those rows only."""
+    say("norm large")
+    T, H = 300000, 7168
+    assert T * H > 2 ** 31
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[-50:] = bf16(50, H, seed=81)
+    gamma = bf16(H, seed=82)
+    tail = x[-50:].contiguous()
+    out, _, rstd = M.moonep_rmsnorm(x, gamma)
+    few, _, few_rstd = M.moonep_rmsnorm(tail, gamma)
+    assert torch.equal(out[-50:], few) and torch.equal(rstd[-50:], few_rstd) and (out[:-50] == 0).all()
+    rows, _, _ = M.moonep_rmsnorm_q8(x, gamma)
+    few_rows, _, _ = M.moonep_rmsnorm_q8(tail, gamma)
+    assert torch.equal(rows[-50:], few_rows)
+    back = M.moonep_q8_unpack(rows, H)
+    assert torch.equal(back[-50:], M.moonep_q8_unpack(few_rows, H)) and (back[:-50] == 0).all()
+    del rows, back
+    g_x, g_gamma = M.moonep_rmsnorm_bwd(out, x, gamma, rstd)
+    few_g, few_gamma = M.moonep_rmsnorm_bwd(few, tail, gamma, few_rstd)
+    assert torch.equal(g_x[-50:], few_g) and (g_x[:-50] == 0).all()
+    # the rows before add zeros, in another order of at most 50 nonzero terms each
+    n = tail.double() * few_rstd.double()[:, None]
+    mag = (few.double() * n).abs().sum(0)
+    assert ((g_gamma.double() - few_gamma.double()).abs() <= 2 * 52 * 2.0 ** -24 * mag).all()
+    torch.cuda.synchronize()
