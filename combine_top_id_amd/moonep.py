@@ -408,7 +408,8 @@ def _bytes(n):
 
 def _on_its_stream(f):
     """f, allocating what it is not given on the stream that it is told to use: memory of
-    another stream could be handed on there (a workspace at once) while the call still runs."""
+    another stream could be handed on there (a workspace at once) while the call still runs.
+    The stream is given by its name."""
     @functools.wraps(f)
     def call(*args, stream=None, **kwargs):
         if stream is None:
@@ -452,7 +453,7 @@ def _act(act):
 
 @_on_its_stream
 def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=False, h=None, gu=None,
-                      y=None, stream=None):
+                      y=None, *, stream=None):
     """The gated feed-forward experts: y[row] = Wd (act(Wg x) * (Wu x)) with x = recv[row] and
     the weights of the row's group.  recv bf16 [R*NvS, H]; home_w bf16 [E, W_el], an
     expert's slab being gate [I, H], up [I, H], down [H, I]; slot_w bf16 [R, slots, W_el].
@@ -475,7 +476,7 @@ def moonep_expert_ffn(plan: Plan, recv, home_w, slot_w, I, act="silu", save=Fals
 
 @_on_its_stream
 def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu", g_gu=None,
-                               g_recv=None, stream=None):
+                               g_recv=None, *, stream=None):
     """Gradient of moonep_expert_ffn with respect to the rows, from g_y bf16 [R*NvS, H] and the
     saved gu.  Returns (g_recv bf16 [R*NvS, H], g_gu bf16 [R*NvS, 2*I]); g_gu may be gu."""
     D, n = plan.blob.device, plan.sz.recv_rows
@@ -494,7 +495,7 @@ def moonep_expert_ffn_bwd_data(plan: Plan, g_y, gu, home_w, slot_w, I, act="silu
 
 @_on_its_stream
 def moonep_expert_ffn_bwd_weight(plan: Plan, recv, g_y, h, g_gu, home_grad=None, rep_grad=None,
-                                 accumulate=False, stream=None):
+                                 accumulate=False, *, stream=None):
     """Gradient of moonep_expert_ffn with respect to the weights: home_grad fp32 [E, G_el]
     (overwritten, or added to with `accumulate`) and rep_grad fp32 [R, slots, G_el]
     (overwritten in the slots the plan uses), laid out as the weights' slabs;
@@ -545,7 +546,7 @@ def _norm_args(x, gamma, res, h, rstd, stats):
 
 
 @_on_its_stream
-def moonep_rmsnorm(x, gamma, eps=1e-6, res=None, out=None, h=None, rstd=None, stats=True, stream=None):
+def moonep_rmsnorm(x, gamma, eps=1e-6, res=None, out=None, h=None, rstd=None, stats=True, *, stream=None):
     """h = bf16(x + res), out = bf16(h * rstd * gamma), rstd = 1 / sqrt(mean(h^2) + eps), row by
     row.  x, res bf16 [T, H], gamma bf16 [H].  Returns (out, h, rstd): h is x where there is
     no residual and no buffer for it, rstd (fp32 [T]) is None where `stats` is false."""
@@ -563,7 +564,7 @@ def moonep_q8_row_bytes(H):
 
 
 @_on_its_stream
-def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None, stats=True, stream=None):
+def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None, stats=True, *, stream=None):
     """moonep_rmsnorm with its output as 8-bit rows, uint8 [T, moonep_q8_row_bytes(H)].
     `rows.view(torch.bfloat16)` is what moonep_dispatch moves.  Returns (rows, h, rstd)."""
     D, T, H, xp, rp, gp, h, hp, rstd, sp = _norm_args(x, gamma, res, h, rstd, stats)
@@ -573,7 +574,7 @@ def moonep_rmsnorm_q8(x, gamma, eps=1e-6, res=None, rows=None, h=None, rstd=None
 
 
 @_on_its_stream
-def moonep_q8_unpack(rows, H, out=None, stream=None):
+def moonep_q8_unpack(rows, H, out=None, *, stream=None):
     """8-bit rows (uint8 [N, moonep_q8_row_bytes(H)], or the same bytes as bf16 elements, as the
     dispatch returns them) expanded to bf16 [N, H]."""
     rb = moonep_q8_row_bytes(H)
@@ -589,7 +590,8 @@ def moonep_q8_unpack(rows, H, out=None, stream=None):
 
 
 @_on_its_stream
-def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, workspace=None, stream=None):
+def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, workspace=None, *,
+                       stream=None):
     """Backward of the norm from the stored h bf16 [T, H] and rstd fp32 [T]; g_h, if given, is
     the gradient that reaches h past the norm.  Returns (g_x bf16 [T, H], the gradient of x
     and of res; g_gamma fp32 [H])."""

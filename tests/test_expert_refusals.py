@@ -3,6 +3,7 @@ C entries with addresses that are never followed, and the binding with CPU tenso
 the 64-bit references of the GPU tests against differences."""
 
 import ctypes
+import inspect
 import os
 
 import pytest
@@ -175,3 +176,10 @@ def test_reference_gradients_against_differences(kind):
             d = d.view_as(t)
             num = (loss(x + d, w) - loss(x - d, w)) / (2 * e) if t is x else (loss(x, w + d) - loss(x, w - d)) / (2 * e)
             assert abs(num - float(g.reshape(-1)[i])) <= 1e-7 * (1 + abs(num))
+
+
+def test_stream_is_given_by_name():
+    # the binding allocates on it before anything else, so it has to know it from the rest
+    for f in (M.moonep_expert_ffn, M.moonep_expert_ffn_bwd_data, M.moonep_expert_ffn_bwd_weight, M.moonep_rmsnorm,
+              M.moonep_rmsnorm_q8, M.moonep_q8_unpack, M.moonep_rmsnorm_bwd):
+        assert inspect.signature(f).parameters["stream"].kind is inspect.Parameter.KEYWORD_ONLY
