@@ -8,7 +8,7 @@ from .moonep import (moonep_query, moonep_plan, moonep_plan_noalloc, moonep_disp
                      moonep_reduce_grad, moonep_plan_status, moonep_dispatch_bwd,
                      moonep_combine_bwd, moonep_prefetch_weight, moonep_expert_stub,
                      moonep_dispatch_staged, moonep_combine_staged, moonep_expert_ffn,
-                     moonep_expert_ffn_bwd_data, moonep_expert_ffn_bwd_weight, moonep_rmsnorm,
+                     moonep_expert_ffn_bwd_data, moonep_expert_ffn_bwd_weight, moonep_expert_tile, moonep_rmsnorm,
                      moonep_rmsnorm_q8, moonep_q8_row_bytes, moonep_q8_unpack,
                      moonep_rmsnorm_bwd, Plan,
                      Sizes, MoonepError, lib, LIB_PATH, EXPORTS)

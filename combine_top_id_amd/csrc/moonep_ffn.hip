@@ -876,6 +876,7 @@ using Tall = Geometry<256, 128, 4, 2, 3>;
 using Square = Geometry<128, 128, 2, 2, 3>;      // two of 4, as the next
 using Medium = Geometry<128, 64, 2, 2, 3>;
 using Small = Geometry<128, 32, 2, 2, 4>;
+enum Tile { LARGE, TALL, SQUARE, MEDIUM, SMALL };
 
 template <int OP, class G>
 hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
@@ -907,15 +908,14 @@ hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
 //   32 experts, gradient, H 1000, I 680   256:  100,   93,  115,  157
 //    4 experts, gradient, H 1024, I 512  1024:   72,   46,   41,   45
 // (128x128 tiles, two workgroups to a CU, were never more than 3% before the best of these.)
-template <int OP>
-hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
-  const int N = OP == FWD1 ? 2 * a.I : OP == BWD1 ? a.I : a.H;
-  const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
-  const double groups = (double)std::min<int64_t>(a.s.E + a.s.R - 1, a.s.A);
+Tile rows_tile(int op, const moonep_sizes& s, int H, int I) {
+  const int N = op == FWD1 ? 2 * I : op == BWD1 ? I : H;
+  const int K = op == FWD1 || op == BWD1 ? H : op == FWD2 ? I : 2 * I;
+  const double groups = (double)std::min<int64_t>(s.E + s.R - 1, s.A);
   const double weights_us = groups * N * K * 2 / 6e6;
   // us of a step where a workgroup has its CU alone, and where the CU, or the chip, is full
   auto us = [&](int bp, int bq, int wgs, double alone, double full) {
-    const double tiles = std::max(groups, (double)a.s.A / bq + groups / 2) * ((N + bp - 1) / bp);
+    const double tiles = std::max(groups, (double)s.A / bq + groups / 2) * ((N + bp - 1) / bp);
     const double r = tiles / wgs, rounds = r <= 1 ? 1 : r < 4 ? std::ceil(r) : r + 0.5;
     const double t = rounds * ((K + BK - 1) / BK + 4.3) * (tiles <= kCus ? alone : full);
     return std::max(t, weights_us) + 0.24 * t;
@@ -923,10 +923,17 @@ hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
   const double large = us(256, 256, kCus, 1.22, 1.31), tall = us(256, 128, kCus, 0.71, 0.81);
   const double medium = us(128, 64, 2 * kCus, 0.43, 0.62), small = us(128, 32, 2 * kCus, 0.37, 0.48);
   const double least = std::min(std::min(large, tall), std::min(medium, small));
-  if (large == least) return launch_rows_as<OP, Large>(a, 1, st);
-  if (tall == least) return launch_rows_as<OP, Tall>(a, 1, st);
-  if (medium == least) return launch_rows_as<OP, Medium>(a, 2, st);
-  return launch_rows_as<OP, Small>(a, 2, st);
+  return large == least ? LARGE : tall == least ? TALL : medium == least ? MEDIUM : SMALL;
+}
+
+template <int OP>
+hipError_t launch_rows(const FfnArgs& a, hipStream_t st) {
+  switch (rows_tile(OP, a.s, a.H, a.I)) {
+    case LARGE: return launch_rows_as<OP, Large>(a, 1, st);
+    case TALL: return launch_rows_as<OP, Tall>(a, 1, st);
+    case MEDIUM: return launch_rows_as<OP, Medium>(a, 2, st);
+    default: return launch_rows_as<OP, Small>(a, 2, st);
+  }
 }
 
 template <class G, bool NT>
@@ -939,14 +946,26 @@ hipError_t launch_grad_as(const GradArgs& a, int per_cu, hipStream_t st) {
 // tiles of the targets (256x256, 128x128, 128x64, the latter two with two workgroups to a CU):
 //    36: 51.7, 38.1, 30.1     66: 55.6, 37.4, 29.4     84: 23.2, 17.2, 16.9    144: 103.6, 64.2, 83.7
 //   142: 18.4, 12.9, 14.7    228: 26.5, 28.6, 33.8    336: 44.3, 44.9, 50.6    912: 57.9, 62.7, 76.7
-hipError_t launch_grad(const GradArgs& a, hipStream_t st) {
+Tile grad_tile(const moonep_sizes& s, int H, int I) {
   auto of = [](int64_t n) { return (n + 255) / 256; };
-  const int64_t targets = a.s.E + std::min<int64_t>(a.s.R - 1, (int64_t)a.s.R * a.s.slots);
-  const int64_t tiles = targets * (of(a.H) * of(2 * a.I) + of(a.I) * of(a.H));
-  if (tiles <= kCus / 3) return launch_grad_as<Medium, false>(a, 2, st);
-  if (tiles <= kCus * 5 / 8) return launch_grad_as<Square, false>(a, 2, st);
-  if ((int64_t)a.s.E * 12 * a.I * a.H > kLastLevelCacheBytes) return launch_grad_as<Large, true>(a, 1, st);
-  return launch_grad_as<Large, false>(a, 1, st);
+  const int64_t targets = s.E + std::min<int64_t>(s.R - 1, (int64_t)s.R * s.slots);
+  const int64_t tiles = targets * (of(H) * of(2 * I) + of(I) * of(H));
+  return tiles <= kCus / 3 ? MEDIUM : tiles <= kCus * 5 / 8 ? SQUARE : LARGE;
+}
+
+// Whether the gradients pass the caches by: 256x256 tiles only (see grad_kernel).
+bool grad_passes_caches(const moonep_sizes& s, int H, int I) {
+  return grad_tile(s, H, I) == LARGE && (int64_t)s.E * 12 * I * H > kLastLevelCacheBytes;
+}
+
+hipError_t launch_grad(const GradArgs& a, hipStream_t st) {
+  switch (grad_tile(a.s, a.H, a.I)) {
+    case MEDIUM: return launch_grad_as<Medium, false>(a, 2, st);
+    case SQUARE: return launch_grad_as<Square, false>(a, 2, st);
+    default: break;
+  }
+  return grad_passes_caches(a.s, a.H, a.I) ? launch_grad_as<Large, true>(a, 1, st)
+                                           : launch_grad_as<Large, false>(a, 1, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -970,6 +989,20 @@ int check_ffn(const moonep_plan_desc* d, int H, int I) {
 using namespace moonep;
 
 extern "C" {
+
+int moonep_expert_tile(const moonep_plan_desc* plan, int H, int I, int product, int32_t tile[3]) {
+  const int rc = check_ffn(plan, H, I);
+  if (rc != MOONEP_OK) return rc;
+  if (!tile || product < MOONEP_PRODUCT_GATE_UP || product > MOONEP_PRODUCT_G_WEIGHTS) return MOONEP_EINVAL;
+  static_assert(FWD1 == MOONEP_PRODUCT_GATE_UP && FWD2 == MOONEP_PRODUCT_DOWN && BWD1 == MOONEP_PRODUCT_G_GATE_UP &&
+                BWD2 == MOONEP_PRODUCT_G_ROWS);
+  const bool grad = product == MOONEP_PRODUCT_G_WEIGHTS;
+  const Tile t = grad ? grad_tile(plan->sz, H, I) : rows_tile(product, plan->sz, H, I);
+  tile[0] = t == LARGE || t == TALL ? 256 : 128;
+  tile[1] = t == LARGE ? 256 : t == MEDIUM ? 64 : t == SMALL ? 32 : 128;
+  tile[2] = grad && grad_passes_caches(plan->sz, H, I);
+  return MOONEP_OK;
+}
 
 int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H, int I, int act,
                       const uint16_t* home_w, const uint16_t* slot_w, int64_t W_el, uint16_t* gu,

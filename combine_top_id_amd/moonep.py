@@ -73,6 +73,7 @@ def lib():
     L.moonep_expert_ffn.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp, vp]
     L.moonep_expert_ffn_bwd_data.argtypes = [PD, vp, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp]
     L.moonep_expert_ffn_bwd_weight.argtypes = [PD, vp, vp, vp, vp, i32, i32, vp, vp, i64, i32, vp]
+    L.moonep_expert_tile.argtypes = [PD, i32, i32, i32, ctypes.POINTER(ctypes.c_int32)]
     L.moonep_rmsnorm.argtypes = [vp, vp, vp, f32, i64, i32, vp, vp, vp, vp]
     L.moonep_rmsnorm_q8.argtypes = [vp, vp, vp, f32, i64, i32, vp, vp, vp, vp]
     L.moonep_q8_unpack.argtypes = [vp, i64, i32, vp, vp]
@@ -89,8 +90,8 @@ def lib():
               "moonep_reduce_grad", "moonep_plan_status", "moonep_dispatch_bwd",
               "moonep_combine_bwd", "moonep_prefetch_weight", "moonep_expert_stub",
               "moonep_dispatch_staged", "moonep_combine_staged", "moonep_expert_ffn",
-              "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_rmsnorm",
-              "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd"):
+              "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_expert_tile",
+              "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -102,10 +103,11 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
            "moonep_dispatch_bwd", "moonep_combine_bwd", "moonep_prefetch_weight",
            "moonep_expert_stub", "moonep_dispatch_staged", "moonep_combine_staged",
            "moonep_expert_ffn", "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight",
-           "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
+           "moonep_expert_tile", "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
            "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd")
 
 ACTIVATIONS = {"silu": 0, "gelu": 1}
+PRODUCTS = ("gate_up", "down", "g_gate_up", "g_rows", "g_weights")
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
@@ -519,6 +521,17 @@ def moonep_expert_ffn_bwd_weight(plan: Plan, recv, g_y, h, g_gu, home_grad=None,
     _run(lib().moonep_expert_ffn_bwd_weight, D, ctypes.byref(plan.desc), rp, yp, hp, gp, H, I, wp, sp, G_el,
          int(bool(accumulate)), _stream(stream, D))
     return home_grad, rep_grad
+
+
+def moonep_expert_tile(plan: Plan, H, I, product):
+    """The tile that a product of the experts' calls ("gate_up" or "down" of the forward pass,
+    "g_gate_up" or "g_rows" of the rows' gradient, "g_weights") is computed in: results along
+    an output row, output rows, and whether the results are written past the caches."""
+    if product not in PRODUCTS:
+        raise MoonepError(f"product must be one of {PRODUCTS}, got {product!r}")
+    tile = (ctypes.c_int32 * 3)()
+    _check(lib().moonep_expert_tile(ctypes.byref(plan.desc), H, I, PRODUCTS.index(product), tile))
+    return tile[0], tile[1], bool(tile[2])
 
 
 def _norm_args(x, gamma, res, h, rstd, stats):

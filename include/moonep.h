@@ -54,6 +54,12 @@ extern "C" {
 #define MOONEP_MAX_NORM 32768    /* hidden size of a normed row                         */
 #define MOONEP_ACT_SILU 0        /* z / (1 + e^-z)                                      */
 #define MOONEP_ACT_GELU 1        /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2     */
+/* the matrix products of the experts' calls (moonep_expert_tile)                      */
+#define MOONEP_PRODUCT_GATE_UP 0   /* moonep_expert_ffn: gate and up, with the activation */
+#define MOONEP_PRODUCT_DOWN 1      /* moonep_expert_ffn: y                                */
+#define MOONEP_PRODUCT_G_GATE_UP 2 /* moonep_expert_ffn_bwd_data: g_gu                    */
+#define MOONEP_PRODUCT_G_ROWS 3    /* moonep_expert_ffn_bwd_data: g_recv                  */
+#define MOONEP_PRODUCT_G_WEIGHTS 4 /* moonep_expert_ffn_bwd_weight                        */
 /* largest planning workspace moonep_plan_noalloc serves from its static device array */
 #define MOONEP_NOALLOC_WORKSPACE_MAX (8 << 20)
 
@@ -317,6 +323,14 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
                                  const uint16_t* g_y, const uint16_t* h, const uint16_t* g_gu,
                                  int H, int I, float* home_grad, float* rep_grad, int64_t G_el,
                                  int accumulate, hipStream_t stream);
+
+/* The tile that a product of the experts' calls is computed in for these sizes, for
+ * profiles and for tests that mean a certain one.  Host only.
+ *   product  MOONEP_PRODUCT_*
+ *   tile     host int32 [3]: results along an output row (of gate and up, half of them each),
+ *            output rows, and 1 where results are written past the caches, else 0
+ * Errors of plan, H and I as in moonep_expert_ffn; EINVAL for another product. */
+int moonep_expert_tile(const moonep_plan_desc* plan, int H, int I, int product, int32_t tile[3]);
 
 /* The root-mean-square norm in front of the experts, with the residual's addition, over T
  * rows (any T, also 0, when nothing is written):
