@@ -983,6 +983,17 @@ int check_ffn(const moonep_plan_desc* d, int H, int I) {
   return MOONEP_OK;
 }
 
+// Tiles of other columns still read the rows of one that is done, and other workgroups the weights:
+// an output that overlapped either would change what they read.  All are known to be aligned.
+Span plan_span(const moonep_plan_desc* d) { return span(d->dev, 1, d->sz.plan_bytes); }
+Span rows_span(const moonep_plan_desc* d, const uint16_t* p, int n) { return span(p, d->sz.recv_rows, 2ll * n); }
+Span home_span(const moonep_plan_desc* d, const void* p, int64_t pitch, int H, int I, int elem_bytes) {
+  return slabs(p, d->sz.E, pitch, 3ll * I * H, elem_bytes);
+}
+Span slot_span(const moonep_plan_desc* d, const void* p, int64_t pitch, int H, int I, int elem_bytes) {
+  return slabs(p, (int64_t)d->sz.R * d->sz.slots, pitch, 3ll * I * H, elem_bytes);
+}
+
 }  // namespace
 }  // namespace moonep
 
@@ -1015,6 +1026,11 @@ int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H,
   if (!aligned(recv, 16) || !aligned(home_w, 16) || !aligned(slot_w, 16) || !aligned(gu, 16) ||
       !aligned(h, 16) || !aligned(y, 16))
     return MOONEP_EALIGN;
+  const Span pl = plan_span(plan), x = rows_span(plan, recv, H), hw = home_span(plan, home_w, W_el, H, I, 2),
+             sw = slot_span(plan, slot_w, W_el, H, I, 2);
+  const Span go = rows_span(plan, gu, 2 * I), ho = rows_span(plan, h, I), yo = rows_span(plan, y, H);
+  if (overlap(go, {pl, x, hw, sw, ho, yo}) || overlap(ho, {pl, x, hw, sw, yo}) || overlap(yo, {pl, x, hw, sw}))
+    return MOONEP_EINVAL;
   FfnArgs a{};
   a.plan = static_cast<const int32_t*>(plan->dev);
   a.s = plan->sz;
@@ -1040,6 +1056,11 @@ int moonep_expert_ffn_bwd_data(const moonep_plan_desc* plan, const uint16_t* g_y
   if (!aligned(g_y, 16) || !aligned(gu, 16) || !aligned(home_w, 16) || !aligned(slot_w, 16) ||
       !aligned(g_gu, 16) || !aligned(g_recv, 16))
     return MOONEP_EALIGN;
+  const Span pl = plan_span(plan), gy = rows_span(plan, g_y, H), in = rows_span(plan, gu, 2 * I),
+             hw = home_span(plan, home_w, W_el, H, I, 2), sw = slot_span(plan, slot_w, W_el, H, I, 2);
+  const Span go = rows_span(plan, g_gu, 2 * I), ro = rows_span(plan, g_recv, H);
+  if (overlap(go, {pl, gy, hw, sw, ro}) || (g_gu != gu && overlap(go, in)) || overlap(ro, {pl, gy, in, hw, sw}))
+    return MOONEP_EINVAL;
   FfnArgs a{};
   a.plan = static_cast<const int32_t*>(plan->dev);
   a.s = plan->sz;
@@ -1065,6 +1086,10 @@ int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* r
   if (!aligned(recv, 16) || !aligned(g_y, 16) || !aligned(h, 16) || !aligned(g_gu, 16) ||
       !aligned(home_grad, 16) || !aligned(rep_grad, 16))
     return MOONEP_EALIGN;
+  const Span pl = plan_span(plan), x = rows_span(plan, recv, H), gy = rows_span(plan, g_y, H),
+             hh = rows_span(plan, h, I), gg = rows_span(plan, g_gu, 2 * I);
+  const Span ho = home_span(plan, home_grad, G_el, H, I, 4), ro = slot_span(plan, rep_grad, G_el, H, I, 4);
+  if (overlap(ho, {pl, x, gy, hh, gg, ro}) || overlap(ro, {pl, x, gy, hh, gg})) return MOONEP_EINVAL;
   GradArgs a{};
   a.plan = static_cast<const int32_t*>(plan->dev);
   a.s = plan->sz;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <hip/hip_runtime.h>
 
 #include "moonep.h"
@@ -100,6 +101,30 @@ inline int check_desc(const moonep_plan_desc* d) {
     return MOONEP_EPLAN;
   if (std::memcmp(&s, &d->sz, sizeof(s)) != 0) return MOONEP_EPLAN;
   return MOONEP_OK;
+}
+
+// Memory that a call is given, from `p` on; nothing where that is null.
+struct Span {
+  const void* p;
+  unsigned __int128 bytes;      // of a pitch up to 2^63 - 1 too
+};
+inline Span span(const void* p, int64_t rows, int64_t row_bytes) {
+  return {p, (unsigned __int128)rows * (uint64_t)row_bytes};
+}
+// `n` slabs of `el` elements, `pitch` elements from each to the next.
+inline Span slabs(const void* p, int64_t n, int64_t pitch, int64_t el, int elem_bytes) {
+  if (n <= 0) return {nullptr, 0};
+  return {p, ((unsigned __int128)(n - 1) * (uint64_t)pitch + (uint64_t)el) * elem_bytes};
+}
+inline bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p) return false;
+  const unsigned __int128 x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+inline bool overlap(const Span& a, std::initializer_list<Span> others) {
+  for (const Span& b : others)
+    if (overlap(a, b)) return true;
+  return false;
 }
 
 // chunks per map wave and map sub-blocks per histogram wave

@@ -285,8 +285,8 @@ int moonep_expert_stub(const moonep_plan_desc* plan, const int32_t* topk_ids,
  *   y       device bf16 [R*NvS, H]
  * H and I are multiples of 8, at most MOONEP_MAX_FFN, with (I + 256) * H < 2^30; W_el is a
  * multiple of 8; all pointers 16-byte aligned.  Padding rows of recv are not read and those
- * of gu, h and y not written.  No output may overlap an input or another output.  EHIP can
- * follow the first of the two launches.  Deterministic. */
+ * of gu, h and y not written.  No output may overlap an input, the plan or another output
+ * (EINVAL).  EHIP can follow the first of the two launches.  Deterministic. */
 int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H, int I, int act,
                       const uint16_t* home_w, const uint16_t* slot_w, int64_t W_el, uint16_t* gu,
                       uint16_t* h, uint16_t* y, hipStream_t stream);
@@ -300,7 +300,7 @@ int moonep_expert_ffn(const moonep_plan_desc* plan, const uint16_t* recv, int H,
  *   g_y     device bf16 [R*NvS, H]      gu      device bf16 [R*NvS, 2*I]
  *   g_gu    device bf16 [R*NvS, 2*I], may be gu itself (in place)
  *   g_recv  device bf16 [R*NvS, H]
- * Weights, sizes, padding rows and errors as in moonep_expert_ffn. */
+ * Weights, sizes, padding rows, overlaps (but g_gu == gu) and errors as in moonep_expert_ffn. */
 int moonep_expert_ffn_bwd_data(const moonep_plan_desc* plan, const uint16_t* g_y,
                                const uint16_t* gu, int H, int I, int act, const uint16_t* home_w,
                                const uint16_t* slot_w, int64_t W_el, uint16_t* g_gu,
@@ -318,7 +318,7 @@ int moonep_expert_ffn_bwd_data(const moonep_plan_desc* plan, const uint16_t* g_y
  *   accumulate 0: home_grad is overwritten (with zeros for an expert without rows);
  *              1: the sums are added to it.  rep_grad is overwritten either way.
  * Of a slab, the first 3*I*H elements are written.  H and I multiples of 8, G_el of 4; all
- * pointers 16-byte aligned.  Deterministic. */
+ * pointers 16-byte aligned; overlaps as in moonep_expert_ffn.  Deterministic. */
 int moonep_expert_ffn_bwd_weight(const moonep_plan_desc* plan, const uint16_t* recv,
                                  const uint16_t* g_y, const uint16_t* h, const uint16_t* g_gu,
                                  int H, int I, float* home_grad, float* rep_grad, int64_t G_el,
