@@ -117,7 +117,7 @@ inline Span slabs(const void* p, int64_t n, int64_t pitch, int64_t el, int elem_
   return {p, ((unsigned __int128)(n - 1) * (uint64_t)pitch + (uint64_t)el) * elem_bytes};
 }
 inline bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p) return false;
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
   const unsigned __int128 x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
   return x < y + b.bytes && y < x + a.bytes;
 }

@@ -327,6 +327,13 @@ int norm(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float ep
   if (!aligned(x, 16) || !aligned(res, 16) || !aligned(gamma, 16) || !aligned(out, 16) ||
       !aligned(h_out, 16) || !aligned(rstd, 4))
     return MOONEP_EALIGN;
+  // A workgroup has read its row when it writes it, so h may be x or res.  Anything else that
+  // overlaps would be written before another workgroup reads it, or be lost to the backward pass.
+  const Span xs = span(x, T, 2ll * H), rs = span(res, T, 2ll * H), gs = span(gamma, 1, 2ll * H);
+  const Span os = span(out, T, out_row), hs = span(h_out, T, 2ll * H), ss = span(rstd, T, 4);
+  if (overlap(os, {xs, rs, gs, hs, ss}) || overlap(ss, {xs, rs, gs, hs}) || overlap(hs, gs) ||
+      (h_out != x && overlap(hs, xs)) || (h_out != res && overlap(hs, rs)))
+    return MOONEP_EINVAL;
   int threads, u;
   shape(H / 8, &threads, &u);
   const bool nt = T * H * 8 > kLastLevelCacheBytes;     // of all rows
@@ -382,6 +389,7 @@ int moonep_q8_unpack(const uint8_t* rows, int64_t N, int H, uint16_t* out, hipSt
   if (N == 0) return MOONEP_OK;
   if (!rows || !out) return MOONEP_EINVAL;
   if (!aligned(rows, 16) || !aligned(out, 16)) return MOONEP_EALIGN;
+  if (overlap(span(rows, N, rb), span(out, N, 2ll * H))) return MOONEP_EINVAL;
   const int64_t blocks = (N * (H / 8) + 255) / 256;
   (void)hipGetLastError();
   hipLaunchKernelGGL(unpack_kernel, dim3(grid_of(blocks, 256)), dim3(256), 0, stream, rows, N, H / 8, rb, reinterpret_cast<u32x4*>(out));
@@ -404,6 +412,12 @@ int moonep_rmsnorm_bwd(const uint16_t* g_out, const uint16_t* h, const uint16_t*
   if (!aligned(g_out, 16) || !aligned(h, 16) || !aligned(gamma, 16) || !aligned(rstd, 4) ||
       !aligned(g_h, 16) || !aligned(workspace, 256) || !aligned(g_x, 16) || !aligned(g_gamma, 16))
     return MOONEP_EALIGN;
+  const Span gs = span(g_out, T, 2ll * H), hs = span(h, T, 2ll * H), ghs = span(g_h, T, 2ll * H);
+  const Span gm = span(gamma, 1, 2ll * H), rs = span(rstd, T, 4);
+  const Span xs = span(g_x, T, 2ll * H), ws = span(workspace, bwd_blocks(T, H), 4ll * H), os = span(g_gamma, 1, 4ll * H);
+  if (overlap(xs, {gm, rs, ws, os}) || (g_x != g_out && overlap(xs, gs)) || (g_x != h && overlap(xs, hs)) ||
+      (g_x != g_h && overlap(xs, ghs)) || overlap(ws, {gs, hs, ghs, gm, rs, os}) || overlap(os, {gs, hs, ghs, gm, rs}))
+    return MOONEP_EINVAL;
   int threads, u;
   shape(H / 8, &threads, &u);
   const int grid = bwd_blocks(T, H);

@@ -340,9 +340,10 @@ int moonep_expert_tile(const moonep_plan_desc* plan, int H, int I, int product, 
  *   gamma   device bf16 [H]
  *   out     device bf16 [T, H]
  *   h       device bf16 [T, H] or NULL: the residual stream after this addition; may be x or
- *           res itself (out may not)
+ *           res itself
  *   rstd    device fp32 [T] or NULL: for the backward pass
- * H % 8 == 0, H <= MOONEP_MAX_NORM, eps >= 0; pointers 16-byte aligned (rstd 4). */
+ * H % 8 == 0, H <= MOONEP_MAX_NORM, eps >= 0; pointers 16-byte aligned (rstd 4).  Other overlaps
+ * of an output with an input or another output are refused (EINVAL). */
 int moonep_rmsnorm(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, float eps,
                    int64_t T, int H, uint16_t* out, uint16_t* h, float* rstd, hipStream_t stream);
 
@@ -362,7 +363,7 @@ int moonep_rmsnorm_q8(const uint16_t* x, const uint16_t* res, const uint16_t* ga
 
 /* Expands N rows in 8 bits (moonep_rmsnorm_q8's, dispatched or not) to bf16 [N, H]:
  * out = code * scale, exact wherever that is a normal bf16 number.  The bytes are taken as
- * they are, so every row may be expanded, mapped or not. */
+ * they are, so every row may be expanded, mapped or not.  out must not overlap rows (EINVAL). */
 int moonep_q8_unpack(const uint8_t* rows, int64_t N, int H, uint16_t* out, hipStream_t stream);
 
 /* Bytes of moonep_rmsnorm_bwd's workspace.  Host only.  Errors as in moonep_rmsnorm. */
@@ -378,7 +379,9 @@ int64_t moonep_rmsnorm_bwd_workspace(int64_t T, int H);
  *              calls whose kernels overlap in time must not share one
  *   g_x        device bf16 [T, H], may be g_out, h or g_h itself
  *   g_gamma    device fp32 [H], overwritten (zeros when T is 0)
- * H % 8 == 0, H <= MOONEP_MAX_NORM; pointers 16-byte aligned (rstd 4).  Deterministic. */
+ * H % 8 == 0, H <= MOONEP_MAX_NORM; pointers 16-byte aligned (rstd 4).  Other overlaps of an output
+ * or the workspace with anything else are refused (EINVAL).  EHIP can follow the first of the two
+ * launches.  Deterministic. */
 int moonep_rmsnorm_bwd(const uint16_t* g_out, const uint16_t* h, const uint16_t* gamma,
                        const float* rstd, const uint16_t* g_h, int64_t T, int H, void* workspace,
                        uint16_t* g_x, float* g_gamma, hipStream_t stream);
