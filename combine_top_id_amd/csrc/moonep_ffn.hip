@@ -116,11 +116,16 @@ __device__ __forceinline__ Seg scalar_seg(const int32_t* plan, const moonep_size
 // for; arrive() is the wait.  m0 holds the LDS address.  gfx9 wants one instruction between
 // writing it and the load, and five between a lane's value read into a scalar register,
 // as which the compiler may bring back a spilled one, and a load that takes it.
+// The compiler warns of m0 in the list because it keeps no value there across the statement:
+// none is, it writes m0 itself right before each use (and these kernels' code has no other).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int OFF>
 __device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to) {
   asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(to), "v"(voff), "s"(rsrc), "i"(OFF) : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 
 // ---------------------------------------------------------------------------------------
 // operand tiles in LDS
