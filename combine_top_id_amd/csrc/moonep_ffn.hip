@@ -902,17 +902,24 @@ hipError_t launch_rows_as(FfnArgs a, int per_cu, hipStream_t st) {
 // time, which is its steps and about four more for its start and end.  Below the weights' own
 // time at 6 TB/s, tiles differ only in what they leave of it, about a quarter of theirs.
 // An expert's group and its replicas end inside a tile: half of one to each group.
-// Measured on MI355X, us for the two launches (Large, Tall, Medium, Small; mean rows of an
-// expert), of which the model takes the best or one within 4%, but for the last two (7%, 14%):
-//   64 experts, forward,  H 7168, I 2048    16: 1129, 1093, 1084, 1072    64: 1153, 1130, 1238, 1662
-//                                          128: 1259, 1292, 1702, 2663   256: 1832, 1800, 2739, 4987
-//   64 experts, gradient, H 2048, I 1024    32:  251,  220,  225,  208    64:  259,  232,  220,  255
-//                                          128:  277,  251,  275,  372   512:  517,  529,  700, 1147
-//   16 experts, forward,  H 2048, I 1024   128:   86,   71,   96,  111   256:   93,  108,  123,  156
-//    4 experts, forward,  H 2048, I 512    128:   52,   44,   28,   26   256:   67,   43,   29,   34
-//   32 experts, gradient, H 1000, I 680   256:  100,   93,  115,  157
-//    4 experts, gradient, H 1024, I 512  1024:   72,   46,   41,   45
-// (128x128 tiles, two workgroups to a CU, were never more than 3% before the best of these.)
+// Measured on MI355X, us of each launch by itself (Large, Tall, Medium, Small; mean rows of an
+// expert).  The model takes the best, or one within 2% of it, but for the two marked *, 6%
+// and 8% behind; R is 8, and 4 for 4 experts.
+//   64 experts, H 7168, I 2048, gate and up   16:  742,  709,  701,  699    64:  754,  734,  758, 1145
+//                                            128:  811,  801, 1126, 1825   256: 1263, 1213, 1856, 3483
+//                               down          16:  374,  372,  373,  366    64:  403,  403,  452,  533
+//                                            128:  438, *466,  545,  810   256:  594,  597,  842, 1497
+//   64 experts, H 2048, I 1024, g_gate, g_up  32:  109,   89,   82,   69    64:  113,   95,   81,   86
+//                                            128:  125,  102,  108,  127   512:  207,  207,  261,  382
+//                               g_recv        32:  134,  125, *135,  138    64:  136,  130,  128,  167
+//                                            128:  147,  135,  173,  239   512:  291,  304,  426,  779
+//   16 experts, H 2048, I 1024, gate and up  128:   51,   38,   49,   51   256:   54,   62,   61,   77
+//                               down         128:   28,   22,   27,   29   256:   29,   33,   33,   43
+//    4 experts, H 2048, I 512,  gate and up  128:   38,   31,   18,   15   256:   49,   30,   18,   20
+//                               down         128: 14.5, 12.6, 10.0, 10.0   256: 17.7, 12.2, 10.4, 13.1
+//   32 experts, H 1000, I 680,  g_gate, g_up 256:   47,   30,   36,   49    g_recv:  40,   44,   51,   70
+//    4 experts, H 1024, I 512,  g_gate, g_up 1024:  44,   27,   19,   21    g_recv:  29,   19,   21,   24
+// (128x128 tiles, two workgroups to a CU, were never the best.)
 Tile rows_tile(int op, const moonep_sizes& s, int H, int I) {
   const int N = op == FWD1 ? 2 * I : op == BWD1 ? I : H;
   const int K = op == FWD1 || op == BWD1 ? H : op == FWD2 ? I : 2 * I;
