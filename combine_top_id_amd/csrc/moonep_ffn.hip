@@ -13,6 +13,13 @@
 // neighbours, and those of lanes that follow each other are too.  A CU writes such runs
 // four times as fast as 16-byte pieces of as many rows as it has lanes (141 and 35 GB/s),
 // and all of an output is written at a tile's end.
+//
+// Roundings.  Sums, activations and their slopes are fp32, and each output is rounded once.  h,
+// g_gate and g_up are outputs and the second products' operands, and so are rounded to bf16 in
+// between: the matrix units multiply bf16 ten times as fast as fp32 (1530 and 153 TF in the
+// library's products), and a second bf16 product of what the rounding leaves would cost
+// its time once more.  y and g_recv are off by 0.0023 to 0.0024 of their size for it, against
+// 0.0017 from one rounding at the end.  The weights' gradient is not rounded at all.
 #include <cmath>
 #include <type_traits>
 
@@ -489,13 +496,16 @@ __device__ __forceinline__ int wave_sums(int v, int lane) {
   return v;
 }
 
-// What bounds it, on MI355X: with hundreds of rows to an expert, power.  512 rows to each of
-// 32 experts, H 7168, I 2048: 1.67 and 0.80 ms, 1170 TF of the formula's products, 1360 with
-// the rows that fill up the groups' last tiles; the matrix units are busy 62% of the time at
+// What bounds it, on MI355X: with hundreds of rows to an expert, power.  1024 rows to each of
+// 32 experts, H 7168, I 2048: 1.68 and 0.81 ms, 1160 TF of the formula's products, 1350 with
+// the rows that fill up the groups' last tiles; the matrix units are busy 60% of the time at
 // 1.7 GHz, where few rows run at 2.4 GHz.  (A 16384 x 8192 x 7168 library product: 88% at
 // 1.48 GHz, 1360 TF.)  With few rows, the weights' stream: 64 rows in 64 experts at one
-// token a rank, 4.0 GB of weights in 428 and 227 us, 6.05 TB/s.  The gradient g_gate, g_up
-// with its four more arrays is between the two: 0.41 ms for 49152 rows, H 2048, I 1408.
+// token a rank, 4.0 GB of weights in 428 and 219 us, 6.1 TB/s.  The gradient g_gate, g_up:
+// its epilogue, which reads two more arrays and writes two, and nothing else runs beside it on
+// the CU.  49152 rows, H 2048, I 1408: 0.41 ms, 1340 to 1400 tiles in six rounds of 69 us, of
+// which the 32 steps take 42.  g_recv of these: 0.51 ms, 1780 to 1860 tiles, of which the last
+// tenth to third of a round is paid as a whole one, and power.
 template <int OP, class G>
 __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
@@ -719,9 +729,12 @@ struct GradArgs {
   int64_t G_el;
 };
 
-// What bounds it, on MI355X: power again, more of which goes into writing.  16384 rows of 16
-// experts, H 7168, I 2048: 1.55 ms, 930 TF, 4.1 GB; the matrix units busy 50% at 1.6 GHz.
-// Few rows: the writes; 21 experts of 73 rows, H 1000, I 680: 200 MB in 49 us.
+// What bounds it, on MI355X: its products and its writes, one after the other, a tile at a time on
+// each CU, both slowed by power.  16384 rows of 16 experts, H 7168, I 2048: 1.58 ms, 914 TF,
+// 50 rounds of 31.6 us, of which 14 steps take about 19 and 67 MB of gradients 10 at 6.5
+// TB/s; the matrix units are busy 50% of the time at 1.6 GHz.
+// Few rows: three steps at least to a tile (what LDS holds), then its writes, with
+// nothing beside them; 21 experts of 73 rows, H 1000, I 680: 200 MB in 49 us.
 // NT: gradients that the last-level cache cannot hold pass it by: 3-6% faster from 0.8 GB on, 10%
 // slower at 0.2 GB.
 template <class G, bool NT>

@@ -55,8 +55,9 @@ constexpr int kThreads = 512;              // of a workgroup, at most
 
 // A workgroup for each row; a thread holds U vectors of 8 elements, read once.  The kernel is
 // an HBM stream: x and the residual in, their sum and the normed row out.  Measured on
-// MI355X at 32768 rows of 7168 in 8 bits (1.65 GB): a workgroup a row, past the caches, 264 us
-// (6.3 TB/s); through them 291 us; 8 workgroups a CU that take rows in turn 307 and 337 us.
+// MI355X at 32768 rows of 7168 in 8 bits (1.65 GB): a workgroup a row, past the caches, 264 to
+// 271 us (6.1 to 6.3 TB/s); through them 291 us; 8 workgroups a CU that take rows in turn 307
+// and 337 us.  In bf16 (1.88 GB) 309 us a call.
 // Where the rows fit in the last-level cache their readers find them there, and nothing
 // passes it by.
 template <int U, int OUT, bool NT>
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const u32x4* x, const u3
 }
 
 // 8 elements a thread: the codes and the block's scale, expanded exactly.  A stream: 33
-// bytes in for 64 out.  A grid as long as the rows, 115 us at 32768 rows of 7168 (6.2
+// bytes in for 64 out.  A grid as long as the rows, 113 to 116 us at 32768 rows of 7168 (6.2
 // TB/s), against 131 us with 16 workgroups a CU that go on.
 __global__ __launch_bounds__(256) void unpack_kernel(const uint8_t* __restrict__ rows, int64_t N,
                                                      int nvec, int64_t row_bytes,
@@ -300,8 +301,8 @@ void shape(int nvec, int* threads, int* u) {
 
 // Workgroups of the backward kernel: one for each CU, or as many short ones as take its place
 // if they have four rows each (each costs a row of partial sums).
-// At 16384 rows of 7168 (940 MB) one measured 152 us (6.2 TB/s) with the column sums, two 162,
-// three without the rows ahead 190.
+// At 16384 rows of 7168 (940 MB) one measured 142 us (6.6 TB/s) and 4 for the column sums; a call
+// took 152 (165 on other boxes) with one, 162 with two, 190 with three without the rows ahead.
 int bwd_blocks(int64_t T, int H) {
   int threads, u;
   shape(H / 8, &threads, &u);
