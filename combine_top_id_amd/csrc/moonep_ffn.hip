@@ -20,29 +20,10 @@
 // library's products), and a second bf16 product of what the rounding leaves would cost
 // its time once more.  y and g_recv are off by 0.0023 to 0.0024 of their size for it, against
 // 0.0017 from one rounding at the end.  The weights' gradient is not rounded at all.
-#include <cmath>
-#include <type_traits>
-
-#include "moonep_internal.h"
+#include "moonep_expert.h"
 
 namespace moonep {
 namespace {
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-#define LDS __attribute__((address_space(3)))
-
-constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every range: reads as zero
-constexpr int kBufferFlags = 0x00020000;   // raw buffer of 32-bit data
-constexpr int kCus = 256;
-constexpr int64_t kLastLevelCacheBytes = 256ll << 20;
-
-constexpr int BK = 64;                     // k of a step
 
 enum Op { FWD1, FWD2, BWD1, BWD2 };
 
@@ -58,244 +39,6 @@ struct FfnArgs {
   uint16_t* out;               // h, y, g_gu or g_recv
   uint16_t* gu_out;            // FWD1: gate and up rows, or null
   int tiles_bound;             // row tiles of any plan of these sizes, at most
-};
-
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// One group of buffer rows that shares its weights.
-struct Seg {
-  int row0, n;
-  int w;                       // home expert, or E + rank * slots + slot
-};
-
-// Segment i of the plan: the E home groups, then the pieces.  Whatever the blob holds, the
-// rows stay inside the buffer and the weights inside their tables.
-template <class Load>
-__device__ __forceinline__ Seg read_seg(const int32_t* plan, const moonep_sizes& s, int i, int np, Load load) {
-  Seg g{0, 0, 0};
-  if (i < s.E) {
-    g.n = load(plan + s.o_keep + i);
-    g.row0 = load(plan + s.o_home_row + i);
-    g.w = i;
-  } else if (i - s.E < np) {
-    const int32_t* pc = plan + s.o_pieces + (int64_t)(i - s.E) * kPieceInts;
-    const int e = load(pc + P_E), r = load(pc + P_R), slot = load(pc + P_SLOT);
-    g.n = load(pc + P_CNT);
-    g.row0 = load(pc + P_ROW0);
-    if (slot >= 0) {
-      g.w = s.E + r * s.slots + slot;
-      if (slot >= s.slots || (unsigned)r >= (unsigned)s.R) g.n = 0;
-    } else {
-      g.w = e;
-      if ((unsigned)e >= (unsigned)s.E) g.n = 0;
-    }
-  }
-  const int rows = (int)s.recv_rows;
-  if (g.n < 0 || g.n > rows || g.row0 < 0 || g.row0 > rows - g.n) g.n = 0;
-  if (g.n == 0) g.row0 = g.w = 0;
-  return g;
-}
-
-__device__ __forceinline__ Seg load_seg(const int32_t* plan, const moonep_sizes& s, int i, int np) {
-  return read_seg(plan, s, i, np, [](const int32_t* p) { return *p; });
-}
-
-__device__ __forceinline__ int piece_count(const int32_t* plan, const moonep_sizes& s) {
-  if (plan[s.o_hdr + H_STATUS] != 0) return 0;
-  return min(max(plan[s.o_hdr + H_NPIECES], 0), s.P_max);
-}
-
-// A word of the plan through the scalar cache, at a uniform address: waited for apart from the
-// loads into LDS.
-__device__ __forceinline__ int scalar(const int32_t* p) {
-  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
-}
-
-// load_seg for a uniform index.
-__device__ __forceinline__ Seg scalar_seg(const int32_t* plan, const moonep_sizes& s, int i, int np) {
-  return read_seg(plan, s, i, np, [](const int32_t* p) { return scalar(p); });
-}
-
-// 16 bytes a lane from the buffer straight into LDS, to `to` + OFF + lane * 16.  In assembly:
-// for the builtin the compiler waits for every such load before any LDS read that it cannot
-// tell apart from it, which here is each one, and the next steps' loads would never be in
-// flight during this step's products.  No register is written, so there is none to wait
-// for; arrive() is the wait.  m0 holds the LDS address.  gfx9 wants one instruction between
-// writing it and the load, and five between a lane's value read into a scalar register,
-// as which the compiler may bring back a spilled one, and a load that takes it.
-// The compiler warns of m0 in the list because it keeps no value there across the statement:
-// none is, it writes m0 itself right before each use (and these kernels' code has no other).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int OFF>
-__device__ __forceinline__ void load_lds(i32x4 rsrc, uint32_t voff, uint32_t to) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(to), "v"(voff), "s"(rsrc), "i"(OFF) : "memory", "scc", "m0");
-}
-#pragma clang diagnostic pop
-
-// ---------------------------------------------------------------------------------------
-// operand tiles in LDS
-// ---------------------------------------------------------------------------------------
-// A step's tile holds BK k of R rows (of P or Q): 64 k are a cache line.  Two forms:
-//   KC  memory is contiguous along k: LDS rows of 64 k, 16-byte chunk c of row r in the place
-//       of chunk c ^ (r & 7): the 16 lanes that read at once hit different banks.
-//   KS  memory is contiguous along the row index: LDS rows (one per k) of R elements, read
-//       transposed.  A fragment of Q is 16 neighbours, and 32-byte unit u of row k is in the
-//       place of u ^ (k & 3 | (k >> 3 & 1) << 2), or of u ^ (k & 3) where R is 64.  A
-//       fragment f of P is every fourth run of four: runs f, f + 4, f + 8 and f + 12 of 64
-//       elements; 16-byte chunk c is in the place of c ^ (k & 1 | (k & 2) << 2): two lanes
-//       to a bank, the best that can be where only half of each 16 bytes is read.
-// Both are filled by 16-byte loads straight into LDS; the swizzle is in each lane's
-// global address, since a wave's load fills 1024 consecutive LDS bytes.
-
-template <int R, bool KS, int NW, bool ISP>
-struct Operand {
-  static constexpr int kBytes = R * BK * 2;
-  static constexpr int kLoads = kBytes / 1024 / NW;
-  static_assert(kLoads >= 1 && kLoads * 1024 * NW == kBytes && (!KS || R >= (ISP ? 128 : 64)));
-  static constexpr int kUnit4 = R >= 128;    // KS: a row of 64 has four units only
-  uint32_t voff[kLoads];
-  int kc;                        // KC: this lane's first k inside a step
-  // the next step to load: its address, the k left from there, and the steps of this tile
-  // from there on (uniform)
-  const char* at;
-  int left, todo;
-  uint32_t ld;                   // bytes of a row in memory
-  uint32_t skip;                 // KS: bytes of the row before `at`
-  i32x4 rs;
-
-  // KC: rowoff(r) is the byte offset of LDS row r in memory, or kOob
-  template <class F>
-  __device__ __forceinline__ void init_kc(int wave, int lane, F rowoff) {
-    const int r = lane >> 3, c = (lane & 7) ^ r;
-    kc = c * 8;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) voff[i] = rowoff((i * NW + wave) * 8 + r) + c * 16;
-  }
-  // KS: columns at or past ncols read as zero
-  __device__ __forceinline__ void init_ks(int wave, int lane, int ncols) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int b = (i * NW + wave) * 1024 + lane * 16;
-      const int k = b / (R * 2), cp = b % (R * 2) / 16;
-      const int c = cp ^ (ISP ? (k & 1) | (k & 2) << 2 : ((k & 3) | (k >> 3 & kUnit4) << 2) << 1);
-      voff[i] = c * 8 < ncols ? k * ld + c * 16 : kOob;
-    }
-  }
-  // Makes the buffer descriptor of the next step and moves on.  Past the end everything is
-  // out of range, and the tile is filled with zeros.
-  __device__ __forceinline__ void next() {
-    const uint64_t p = reinterpret_cast<uint64_t>(at);
-    const int rows = max(min(left, BK), 0);
-    const int range = !KS ? 0x7fffffff : rows ? rows * (int)ld - (int)skip : 0;
-    rs = i32x4{(int)p, (int)(p >> 32) & 0xFFFF, range, kBufferFlags};
-    if (!KS && left < BK) {     // the last k, or none
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) voff[i] |= kc >= left ? kOob : 0;
-    }
-    at += KS ? (uint64_t)ld * BK : BK * 2;
-    left -= BK;
-    --todo;
-  }
-  // load I of the step
-  template <int I, int OFF>
-  __device__ __forceinline__ void load(uint32_t to) const {
-    load_lds<I * NW * 1024 + OFF>(rs, voff[I], to);
-  }
-};
-
-// `v`, of which the compiler cannot know before: what is computed of it stays where it is
-// used, and not in registers that the products need.
-__device__ __forceinline__ int here(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-// This lane's part of the LDS addresses of the fragments from row0 (a multiple of what the wave
-// takes) on, and fragment f (16 rows), k from kk * 32 on, of the tile that `at` adds to it.
-template <int R, bool KS, bool ISP>
-__device__ __forceinline__ int fragment_lane(int row0, int lane) {
-  if constexpr (!KS) return (row0 + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-  const int g = lane >> 4, j = (lane & 15) >> 2, k = (g * 8 + j) * (R * 2);
-  if constexpr (ISP) return k + (((row0 / 8 + (lane & 3) * 2) ^ ((j & 1) | (j & 2) << 2)) << 4);
-  return k + (((row0 / 16) ^ j ^ (R >= 128 ? (g & 1) << 2 : 0)) << 5) + (lane & 3) * 8;
-}
-template <int R, bool KS, bool ISP>
-__device__ __forceinline__ bf16x8 fragment(int at, int f, int kk) {
-  if constexpr (!KS) {
-    return *(const LDS bf16x8*)((at ^ (kk << 6)) + f * 2048);
-  } else {
-    const int x = (ISP ? (at ^ (f >> 1) << 4) + (f & 1) * 8 : at ^ (f << 5)) + kk * 64 * R;
-    union { s16x4 h[2]; bf16x8 v; } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)x);
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS s16x4*)(x + 4 * R * 2));
-    return u.v;
-  }
-}
-
-// Row f * 16 + c of 64 LDS rows of a KC operand P holds row c * 4 + f of memory: lane c's
-// results of the four fragments are neighbours.  With gate and up rows in turn, the first
-// two fragments hold gate rows c * 2 + f, the others the same rows of up.
-__device__ __forceinline__ int p_row(int r) { return (r & ~63) | (r & 15) << 2 | (r >> 4 & 3); }
-__device__ __forceinline__ int p_row_pair(int r) { return (r >> 6) * 32 + ((r & 15) << 1 | (r >> 4 & 1)); }
-
-template <int PF, int QF>
-__device__ __forceinline__ void clear(f32x4 (&acc)[PF][QF]) {
-#pragma unroll
-  for (int p = 0; p < PF; ++p)
-#pragma unroll
-    for (int q = 0; q < QF; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-}
-
-// The tile of workgroup b in round `round` of a grid that is a multiple of 8: workgroups go
-// to the 8 XCDs in turn, so each XCD takes a run of consecutive tiles, which share rows and
-// weights in its L2.
-__device__ __forceinline__ int tile_of(int round, int b, int grid) {
-  return round * grid + (b & 7) * (grid >> 3) + (b >> 3);
-}
-
-// Tile `local` of an n x m grid of tiles: bands of kBand m, n by n within a band, so that 32
-// consecutive tiles are about as many m as n.
-constexpr int kBand = 4;
-__device__ __forceinline__ void band(int local, int m, int n, int* tm, int* tn) {
-  const int b = local / (kBand * n), r = local - b * kBand * n;
-  const int cnt = min(kBand, m - b * kBand);
-  *tm = b * kBand + r % cnt;
-  *tn = r / cnt;
-}
-
-// s_waitcnt with the given vmcnt, and with lgkmcnt(0)
-constexpr int wait_vm_lds(int vm) { return (vm & 15) | (vm >> 4) << 14 | 0x70; }
-
-// Waits until at most VM of this wave's loads are on their way and its LDS reads are done,
-// then for every wave of the workgroup.
-template <int VM>
-__device__ __forceinline__ void arrive() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(wait_vm_lds(VM));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// The wave's own reads from memory have arrived: said here, the compiler does not wait for them
-// later, when the next tile's loads would be waited for with them.
-__device__ __forceinline__ void settled() { __builtin_amdgcn_s_waitcnt(wait_vm_lds(0)); }
-
-template <int N, class F>
-__device__ __forceinline__ void times(F f) {
-  if constexpr (N > 0) {
-    times<N - 1>(f);
-    f(std::integral_constant<int, N - 1>{});
-  }
-}
-
-// A tile's geometry: BP x BQ results by WP x WQ waves; LDS holds the tiles of NB steps of P and
-// NB - 1 of Q.
-template <int BP_, int BQ_, int WP_, int WQ_, int NB_>
-struct Geometry {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NB = NB_, NW = WP * WQ;
-  static constexpr int PF = BP / WP / 16, QF = BQ / WQ / 16;
 };
 
 // The products of one tile after another, without a break between them.  A step is two halves,
@@ -410,61 +153,6 @@ struct Pipe {
   }
 };
 
-__device__ __forceinline__ uint32_t bf2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  bf16x2 v{(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// act(z), and its slope.  SiLU: z s with s = 1 / (1 + e^-z), slope s + z s (1 - s).
-// GELU in its tanh form: z p with p = (1 + tanh(u)) / 2 = 1 / (1 + e^-2u),
-// u = c (z + 0.044715 z^3), slope p + 2 z p (1 - p) u'.  Beyond |z| = 16 p is exactly 0 or
-// 1 in fp32 and u' would overflow, so u is taken of z cut to that range (a NaN stays one).
-__device__ __forceinline__ float act_of(float z, int act, float* slope) {
-  if (act == MOONEP_ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-z));
-    *slope = s + z * s * (1.f - s);
-    return z * s;
-  }
-  const float c = 0.7978845608028654f;
-  const float zc = z < -16.f ? -16.f : z > 16.f ? 16.f : z;
-  const float z2 = zc * zc;
-  const float p = 1.f / (1.f + __expf(-2.f * c * (zc + 0.044715f * zc * z2)));
-  *slope = p + 2.f * zc * p * (1.f - p) * c * (1.f + 0.134145f * z2);
-  return z * p;
-}
-
-// Memory from a tile's first element on, by byte offsets; kOob for what is not to be touched.
-struct Window {
-  __amdgpu_buffer_rsrc_t rs;
-  template <class T>
-  __device__ __forceinline__ explicit Window(T* p)
-      : rs(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, kBufferFlags)) {}
-  __device__ __forceinline__ void store(uint32_t v, uint32_t at) const {
-    __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, 0, 0);
-  }
-  __device__ __forceinline__ void store(u32x2 v, uint32_t at) const {
-    __builtin_amdgcn_raw_buffer_store_b64(v, rs, at, 0, 0);
-  }
-  template <bool NT>
-  __device__ __forceinline__ void store(f32x4 v, uint32_t at) const {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, 0, NT ? 2 : 0);
-  }
-  __device__ __forceinline__ u32x2 load2(uint32_t at) const {
-    return __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-  }
-  __device__ __forceinline__ f32x4 load4(uint32_t at) const {
-    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0));
-  }
-};
-
-template <int CTRL>
-__device__ __forceinline__ float quad_move(float v) {
-  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
-}
-
 // This lane's results i of the four fragments, as four neighbours along p.  For KC that is
 // what they are.  For KS lane (m, e) holds p = m * 16 + f * 4 + e for f = 0 ... 3, and the
 // four lanes of a quad exchange theirs, for m * 16 + e * 4 + f.
@@ -485,16 +173,6 @@ __device__ __forceinline__ f32x4 neighbours(const f32x4 (&acc)[4][QF], int q, in
 // ---------------------------------------------------------------------------------------
 // the row products: forward, and the rows' gradient
 // ---------------------------------------------------------------------------------------
-
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_sums(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
 
 // What bounds it, on MI355X: with hundreds of rows to an expert, power.  1024 rows to each of
 // 32 experts, H 7168, I 2048: 1.68 and 0.81 ms, 1160 TF of the formula's products, 1350 with
@@ -520,72 +198,12 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   const int wp = wave % WP, wq = wave / WP;
   const int32_t* plan = a.plan;
   if (uni(plan[a.s.o_hdr + H_STATUS]) != 0) return;
-  const int np = uni(piece_count(plan, a.s));
-  const int nseg = a.s.E + np;
   const int K = OP == FWD1 || OP == BWD1 ? a.H : OP == FWD2 ? a.I : 2 * a.I;
   const int N = OP == FWD1 || OP == BWD1 ? a.I : a.H;
-  const int nt = (N + BN - 1) / BN;
   const int nk = max((K + BK - 1) / BK, G::NB);      // P loads NB steps ahead, into one more tile only
-
-  // Lane l sums the row tiles of segments [l * per, l * per + per).
-  const int per = (nseg + 63) / 64;
-  int sum = 0;
-  Seg mine{0, 0, 0};                           // the lane's last
-  for (int j = 0; j < per; ++j) {
-    const int i = lane * per + j;
-    if (i < nseg) mine = load_seg(plan, a.s, i, np);
-    if (i < nseg) sum += (mine.n + BQ - 1) / BQ;
-  }
-  sum = wave_sums(sum, lane);
-  const int tiles = min(__builtin_amdgcn_readlane(sum, 63), a.tiles_bound) * nt;
-
-  // Lane l looks up the workgroup's tile of round first + l, each wave on its own: no LDS,
-  // no barrier, and 64 rounds without a wait for memory.
-  int lane_row = -1;                            // first row, or none
-  uint32_t lane_rest = 0;                       // rows - 1, column tile, weight
-  auto look_up = [&](int first, bool held) {
-    const int t = tile_of(first + lane, blockIdx.x, gridDim.x);
-    const int want = t < 0 || t >= tiles ? 0 : t / nt;
-    int l = 0;                                  // the sums that are at most `want`
-#pragma unroll
-    for (int d = 32; d; d /= 2)
-      if (__shfl(sum, l + d - 1) <= want) l += d;
-    int below = __shfl(sum, max(l - 1, 0));
-    below = l ? below : 0;
-    Seg g{0, 0, 0};
-    int mt = 0;
-    if (held && per == 1) {                     // the other lanes hold them all: no second read
-      g = Seg{__shfl(mine.row0, l), __shfl(mine.n, l), __shfl(mine.w, l)};
-      mt = (g.n + BQ - 1) / BQ;
-    } else {
-      for (int j = 0; j < per; ++j) {
-        g = load_seg(plan, a.s, min(l * per + j, nseg - 1), np);
-        mt = (g.n + BQ - 1) / BQ;
-        if (below + mt > want) break;
-        below += mt;
-      }
-    }
-    lane_row = -1;
-    const int local = t - below * nt;
-    if (t >= 0 && t < tiles && local >= 0 && local < mt * nt) {
-      int tm, tn;
-      band(local, mt, nt, &tm, &tn);
-      lane_row = g.row0 + tm * BQ;
-      lane_rest = (uint32_t)(min(g.n - tm * BQ, BQ) - 1) | (uint32_t)tn << 8 | (uint32_t)g.w << 17;
-    }
-    settled();
-  };
-  struct Tile {
-    int row, rows, n0, w;                       // rows 0: none
-  };
-  auto tile = [&](int round) -> Tile {
-    if (round && (round & 63) == 0) look_up(round, false);
-    const int row = __builtin_amdgcn_readlane(lane_row, round & 63);
-    const uint32_t rest = __builtin_amdgcn_readlane(lane_rest, round & 63);
-    if (row < 0) return {0, 0, 0, 0};
-    return {row, (int)(rest & 255) + 1, (int)(rest >> 8 & 511) * BN, (int)(rest >> 17)};
-  };
-  look_up(0, true);
+  RowTiles<BQ> queue(plan, a.s, lane, (N + BN - 1) / BN, a.tiles_bound);
+  using Tile = typename RowTiles<BQ>::Tile;
+  queue.look_up(0, true);
 
   Tiles pipe(smem, wave, lane);
   auto& P = pipe.P;
@@ -593,21 +211,22 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   auto start_p = [&](const Tile& t) {
     const uint16_t* W = t.w < a.s.E ? a.home_w + t.w * a.W_el : a.slot_w + (t.w - a.s.E) * a.W_el;
     if (OP == FWD2 || OP == BWD1) W += 2ll * a.I * a.H;
+    const int n0 = t.tn * BN;
     P.left = K;
     P.todo = nk;
     if constexpr (!KSP) {
       P.ld = K * 2;
       P.skip = 0;
-      P.at = reinterpret_cast<const char*>(W) + (int64_t)t.n0 * P.ld;
+      P.at = reinterpret_cast<const char*>(W) + (int64_t)n0 * P.ld;
       P.init_kc(wave, here(lane), [&](int r) -> uint32_t {
         const int c = PAIR ? p_row_pair(r) : p_row(r);
-        return t.n0 + c < N ? (uint32_t)(c + (PAIR ? (r >> 5 & 1) * a.I : 0)) * P.ld : kOob;
+        return n0 + c < N ? (uint32_t)(c + (PAIR ? (r >> 5 & 1) * a.I : 0)) * P.ld : kOob;
       });
     } else {
       P.ld = N * 2;
-      P.skip = t.n0 * 2;
+      P.skip = n0 * 2;
       P.at = reinterpret_cast<const char*>(W) + P.skip;
-      P.init_ks(wave, here(lane), N - t.n0);
+      P.init_ks(wave, here(lane), N - n0);
     }
   };
   auto start_q = [&](const Tile& t) {
@@ -619,7 +238,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
     Q.init_kc(wave, here(lane), [&](int r) -> uint32_t { return r < t.rows ? r * Q.ld : kOob; });
   };
 
-  Tile cur = tile(0), nxt = tile(1);
+  Tile cur = queue.tile(0), nxt = queue.tile(1);
   if (!cur.rows) return;
   auto more_p = [&] { if (P.todo == 0 && nxt.rows) start_p(nxt); };
   auto more_q = [&] { if (Q.todo == 0 && nxt.rows) start_q(nxt); };
@@ -629,7 +248,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
   for (int round = 1;; ++round) {
     f32x4 acc[PF][QF];
     clear(acc);
-    const int trow = cur.row, tq = cur.rows, tn0 = cur.n0;
+    const int trow = cur.row, tq = cur.rows, tn0 = cur.tn * BN;
     const bool idle = tn0 + wp * (BN / WP) >= N;                    // no columns for this wave
     const int live = idle ? 0 : tq - wq * QF * 16;
     constexpr int kStores = 4 * QF;
@@ -707,7 +326,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void rows_kernel(const FfnArgs a) {
     }
     if (!nxt.rows) break;
     cur = nxt;
-    nxt = tile(round + 1);
+    nxt = queue.tile(round + 1);
   }
   settled();                      // LDS is not given up while loads may still write to it
 #endif
@@ -993,8 +612,6 @@ hipError_t launch_grad(const GradArgs& a, hipStream_t st) {
                                            : launch_grad_as<Large, false>(a, 1, st);
 }
 
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 int check_ffn(const moonep_plan_desc* d, int H, int I) {
   const int rc = check_desc(d);
   if (rc != MOONEP_OK) return rc;
@@ -1010,8 +627,6 @@ int check_ffn(const moonep_plan_desc* d, int H, int I) {
 
 // Tiles of other columns still read the rows of one that is done, and other workgroups the weights:
 // an output that overlapped either would change what they read.  All are known to be aligned.
-Span plan_span(const moonep_plan_desc* d) { return span(d->dev, 1, d->sz.plan_bytes); }
-Span rows_span(const moonep_plan_desc* d, const uint16_t* p, int n) { return span(p, d->sz.recv_rows, 2ll * n); }
 Span home_span(const moonep_plan_desc* d, const void* p, int64_t pitch, int H, int I, int elem_bytes) {
   return slabs(p, d->sz.E, pitch, 3ll * I * H, elem_bytes);
 }
