@@ -79,8 +79,13 @@ def lib():
     L.moonep_q8_unpack.argtypes = [vp, i64, i32, vp, vp]
     L.moonep_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp]
     L.moonep_q8_row_bytes.argtypes = [i32]
+    L.moonep_w4_slab_bytes.argtypes = [i32, i32]
+    L.moonep_w4_pack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
+    L.moonep_w4_unpack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
+    L.moonep_expert_ffn_w4.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp, vp]
+    L.moonep_expert_ffn_w4q8.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp]
     L.moonep_rmsnorm_bwd_workspace.argtypes = [i64, i32]
-    for f in ("moonep_q8_row_bytes", "moonep_rmsnorm_bwd_workspace"):
+    for f in ("moonep_q8_row_bytes", "moonep_rmsnorm_bwd_workspace", "moonep_w4_slab_bytes"):
         getattr(L, f).restype = i64
     L.moonep_plan_status.argtypes = [ctypes.POINTER(PlanDesc), ctypes.POINTER(PlanStats), vp]
     L.moonep_strerror.argtypes = [i32]
@@ -91,7 +96,8 @@ def lib():
               "moonep_combine_bwd", "moonep_prefetch_weight", "moonep_expert_stub",
               "moonep_dispatch_staged", "moonep_combine_staged", "moonep_expert_ffn",
               "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_expert_tile",
-              "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd"):
+              "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd",
+              "moonep_w4_pack", "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -104,7 +110,8 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
            "moonep_expert_stub", "moonep_dispatch_staged", "moonep_combine_staged",
            "moonep_expert_ffn", "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight",
            "moonep_expert_tile", "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
-           "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd")
+           "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd", "moonep_w4_slab_bytes", "moonep_w4_pack",
+           "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8")
 
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 PRODUCTS = ("gate_up", "down", "g_gate_up", "g_rows", "g_weights")
@@ -440,7 +447,7 @@ def _slabs(plan, home, slot, el, dtype, names):
     hp = _dev(home, dtype, names[0], D)
     pitch = home.shape[-1]
     if home.numel() != plan.sz.E * pitch or pitch < el:
-        raise MoonepError(f"{names[0]} must be [E, 3*I*H or more]")
+        raise MoonepError(f"{names[0]} must be [E, {el} or more]")
     n = plan.sz.R * plan.sz.slots * pitch
     if (slot.numel() if slot is not None else 0) != n:
         raise MoonepError(f"{names[1]} must be [R, slots, {pitch}]")
@@ -627,6 +634,86 @@ def moonep_rmsnorm_bwd(g_out, h, gamma, rstd, g_h=None, g_x=None, g_gamma=None, 
         raise MoonepError(f"workspace must hold {need} bytes")
     _run(lib().moonep_rmsnorm_bwd, D, op, hp, gp, sp, ghp, T, H, wp, xp, ggp, _stream(stream, D))
     return g_x, g_gamma.view(H)
+
+
+def moonep_w4_slab_bytes(H, I):
+    """Bytes of an expert's slab in 4 bits."""
+    return _bytes(lib().moonep_w4_slab_bytes(H, I))
+
+
+def _row_pitch(t, dtype, name, device=None):
+    """Device pointer, rows and columns of a two-dimensional `t`."""
+    p = _dev(t, dtype, name, device)
+    if t.dim() != 2:
+        raise MoonepError(f"{name} must have two dimensions")
+    return p, t.shape[0], t.shape[1]
+
+
+@_on_its_stream
+def moonep_w4_pack(w, H, I, out=None, *, stream=None):
+    """bf16 slabs [n, W_el] (gate [I, H], up [I, H], down [H, I], as moonep_expert_ffn takes them) in
+    4 bits with a power of two for 32: uint8 [n, moonep_w4_slab_bytes(H, I)], or `out`, whose
+    rows may be longer.  `out.view(torch.bfloat16)` is what moonep_prefetch_weight moves."""
+    wp, n, W_el = _row_pitch(w, torch.bfloat16, "w")
+    D, need = w.device, moonep_w4_slab_bytes(H, I)
+    if out is None:
+        out = torch.empty(n, need, dtype=torch.uint8, device=D)
+    op, m, pitch = _row_pitch(out, torch.uint8, "out", D)
+    if m != n:
+        raise MoonepError(f"out must be [{n}, {need} or more]")
+    _run(lib().moonep_w4_pack, D, wp, W_el, n, H, I, op, pitch, _stream(stream, D))
+    return out
+
+
+@_on_its_stream
+def moonep_w4_unpack(w4, H, I, out=None, *, stream=None):
+    """Slabs in 4 bits (uint8 [n, W_bytes]) expanded exactly to bf16 [n, 3*I*H], or `out`, whose
+    rows may be longer: what moonep_expert_ffn and moonep_expert_ffn_bwd_data take."""
+    wp, n, pitch = _row_pitch(w4, torch.uint8, "w4")
+    D = w4.device
+    if out is None:
+        out = torch.empty(n, 3 * I * H, dtype=torch.bfloat16, device=D)
+    op, m, W_el = _row_pitch(out, torch.bfloat16, "out", D)
+    if m != n:
+        raise MoonepError(f"out must be [{n}, {3 * I * H} or more]")
+    _run(lib().moonep_w4_unpack, D, wp, pitch, n, H, I, op, W_el, _stream(stream, D))
+    return out
+
+
+@_on_its_stream
+def moonep_expert_ffn_w4(plan: Plan, recv, home_w4, slot_w4, I, act="silu", save=False, h=None, gu=None,
+                         y=None, *, stream=None):
+    """moonep_expert_ffn with weights in 4 bits: home_w4 uint8 [E, W_bytes] (moonep_w4_pack's), slot_w4
+    uint8 [R, slots, W_bytes].  Rows, results and what is saved are as there."""
+    D, n = plan.blob.device, plan.sz.recv_rows
+    H = recv.shape[-1]
+    _, rp = _rows(recv, torch.bfloat16, "recv", n, H, D, recv)
+    wp, sp, pitch = _slabs(plan, home_w4, slot_w4, moonep_w4_slab_bytes(H, I), torch.uint8, ("home_w4", "slot_w4"))
+    h, hp = _rows(h, torch.bfloat16, "h", n, I, D, recv)
+    y, yp = _rows(y, torch.bfloat16, "y", n, H, D, recv)
+    gp = None
+    if save or gu is not None:
+        gu, gp = _rows(gu, torch.bfloat16, "gu", n, 2 * I, D, recv)
+    _run(lib().moonep_expert_ffn_w4, D, ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, pitch, gp, hp, yp,
+         _stream(stream, D))
+    return y, h, gu
+
+
+@_on_its_stream
+def moonep_expert_ffn_w4q8(plan: Plan, rows, home_w4, slot_w4, H, I, act="silu", h=None, y=None, *, stream=None):
+    """moonep_expert_ffn with weights in 4 bits and rows in 8: rows uint8 [R*NvS, moonep_q8_row_bytes(H)]
+    (moonep_rmsnorm_q8's, dispatched; the same bytes as bf16 elements are taken too).  Returns (y bf16
+    [R*NvS, H], h uint8 [R*NvS, moonep_q8_row_bytes(I)])."""
+    D, n = plan.blob.device, plan.sz.recv_rows
+    if isinstance(rows, torch.Tensor) and rows.dtype == torch.bfloat16 and rows.is_contiguous():
+        rows = rows.view(torch.uint8)
+    _, rp = _rows(rows, torch.uint8, "rows", n, moonep_q8_row_bytes(H), D, rows)
+    wp, sp, pitch = _slabs(plan, home_w4, slot_w4, moonep_w4_slab_bytes(H, I), torch.uint8, ("home_w4", "slot_w4"))
+    h, hp = _rows(h, torch.uint8, "h", n, moonep_q8_row_bytes(I), D, rows)
+    y, yp = _rows(y, torch.bfloat16, "y", n, H, D, rows)
+    _run(lib().moonep_expert_ffn_w4q8, D, ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, pitch, hp, yp,
+         _stream(stream, D))
+    return y, h
 
 
 def moonep_plan_status(plan: Plan, stream=None) -> dict:
