@@ -7,7 +7,7 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["moonep_api.hip", "moonep_plan.hip", "moonep_move.hip", "moonep_ffn.hip",
-           "moonep_norm.hip", "moonep_w4.hip"]
+           "moonep_norm.hip", "moonep_w4.hip", "moonep_router.hip"]
 STREAM_SOURCES = ["moonep_streams.hip"]
 
 HIPCC_FLAGS = [

@@ -79,6 +79,8 @@ def lib():
     L.moonep_q8_unpack.argtypes = [vp, i64, i32, vp, vp]
     L.moonep_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp]
     L.moonep_q8_row_bytes.argtypes = [i32]
+    L.moonep_router.argtypes = [vp, i32, vp, i64, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]
+    L.moonep_router_bwd.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, i32, f32, vp, vp]
     L.moonep_w4_slab_bytes.argtypes = [i32, i32]
     L.moonep_w4_pack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
     L.moonep_w4_unpack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
@@ -97,7 +99,8 @@ def lib():
               "moonep_dispatch_staged", "moonep_combine_staged", "moonep_expert_ffn",
               "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_expert_tile",
               "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd",
-              "moonep_w4_pack", "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8"):
+              "moonep_w4_pack", "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8",
+              "moonep_router", "moonep_router_bwd"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -111,9 +114,11 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
            "moonep_expert_ffn", "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight",
            "moonep_expert_tile", "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
            "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd", "moonep_w4_slab_bytes", "moonep_w4_pack",
-           "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8")
+           "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8", "moonep_router", "moonep_router_bwd")
 
 ACTIVATIONS = {"silu": 0, "gelu": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+LOGITS = {torch.float32: 0, torch.bfloat16: 1}
 PRODUCTS = ("gate_up", "down", "g_gate_up", "g_rows", "g_weights")
 
 
@@ -714,6 +719,57 @@ def moonep_expert_ffn_w4q8(plan: Plan, rows, home_w4, slot_w4, H, I, act="silu",
     _run(lib().moonep_expert_ffn_w4q8, D, ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, pitch, hp, yp,
          _stream(stream, D))
     return y, h
+
+
+def _logits(logits, score):
+    """Device pointer, type, rows, columns and the score's code of a router's logits."""
+    kind = LOGITS.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    lp = _dev(logits, logits.dtype if kind is not None else torch.float32, "logits")
+    if logits.dim() != 2:
+        raise MoonepError("logits must be [T, E]")
+    if score not in SCORES:
+        raise MoonepError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return lp, kind, logits.shape[0], logits.shape[1], SCORES[score]
+
+
+@_on_its_stream
+def moonep_router(logits, K, bias=None, score="softmax", groups=1, top_groups=1, normalize=True, scale=1.0,
+                  ids=None, w=None, *, stream=None):
+    """The K experts of each token and their weights, as moonep_plan takes them: (ids int32 [T, K], w fp32
+    [T, K]) from logits fp32 or bf16 [T, E].  Experts are chosen by score + bias (fp32 [E]) among the
+    top_groups best of `groups` groups; weights are the scores, divided by their sum with
+    `normalize`, times `scale`."""
+    lp, kind, T, E, code = _logits(logits, score)
+    D = logits.device
+    bp = None
+    if bias is not None:
+        bp = _dev(bias, torch.float32, "bias", D)
+        if bias.numel() != E:
+            raise MoonepError("bias must be [E]")
+    ids, ip = _rows(ids, torch.int32, "ids", T, K, D, logits)
+    w, wp = _rows(w, torch.float32, "w", T, K, D, logits)
+    _run(lib().moonep_router, D, lp, kind, bp, T, E, K, code, groups, top_groups, int(bool(normalize)), scale, ip, wp,
+         _stream(stream, D))
+    return ids, w
+
+
+@_on_its_stream
+def moonep_router_bwd(logits, ids, g_w, score="softmax", normalize=True, scale=1.0, g_logits=None, *, stream=None):
+    """The logits' gradient [T, E], of their type, from the weights' g_w fp32 [T, K] (moonep_combine_bwd's dw),
+    for the ids int32 [T, K] that moonep_router chose."""
+    lp, kind, T, E, code = _logits(logits, score)
+    D = logits.device
+    ip = _dev(ids, torch.int32, "ids", D)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise MoonepError("ids must be [T, K]")
+    K = ids.shape[1]
+    gp = _rows(g_w, torch.float32, "g_w", T, K, D, logits)[1] if g_w is not None else None
+    if gp is None:
+        raise MoonepError("g_w must be a GPU tensor")
+    g_logits, op = _rows(g_logits, logits.dtype, "g_logits", T, E, D, logits)
+    _run(lib().moonep_router_bwd, D, lp, kind, ip, gp, T, E, K, code, int(bool(normalize)), scale, op,
+         _stream(stream, D))
+    return g_logits
 
 
 def moonep_plan_status(plan: Plan, stream=None) -> dict:

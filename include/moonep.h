@@ -56,6 +56,11 @@ extern "C" {
 #define MOONEP_MAX_NORM 32768    /* hidden size of a normed row                         */
 #define MOONEP_ACT_SILU 0        /* z / (1 + e^-z)                                      */
 #define MOONEP_ACT_GELU 1        /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2     */
+#define MOONEP_F32 0             /* types of the router's logits                        */
+#define MOONEP_BF16 1
+#define MOONEP_SCORE_SOFTMAX 0   /* the router's scores of an expert's logit            */
+#define MOONEP_SCORE_SIGMOID 1
+#define MOONEP_MAX_GROUPS 64     /* the router's groups of experts                      */
 /* the matrix products of the experts' calls (moonep_expert_tile)                      */
 #define MOONEP_PRODUCT_GATE_UP 0   /* moonep_expert_ffn: gate and up, with the activation */
 #define MOONEP_PRODUCT_DOWN 1      /* moonep_expert_ffn: y                                */
@@ -440,6 +445,39 @@ int moonep_expert_ffn_w4(const moonep_plan_desc* plan, const uint16_t* recv, int
 int moonep_expert_ffn_w4q8(const moonep_plan_desc* plan, const uint8_t* rows, int H, int I, int act,
                            const uint8_t* home_w4, const uint8_t* slot_w4, int64_t W_bytes, uint8_t* h,
                            uint16_t* y, hipStream_t stream);
+
+/* The router in front of the plan, over T tokens (any T, also 0, when nothing is written): what it
+ * writes is what moonep_plan takes.
+ *   s = softmax(l) or sigmoid(l) of a token's E logits;  key = s + bias
+ *   The experts are in `groups` groups of E / groups neighbours.  A group's score is the sum of its
+ *   two largest keys; the top_groups best groups are kept (1 of 1: all experts).
+ *   topk_ids  the K experts of these groups with the largest keys, largest first
+ *   topk_w    scale * s of each (fp32, without the bias), divided by their sum if normalize is 1
+ * Equal keys and equal group scores go to the lowest index.  Keys are compared in 64 bits.
+ * A logit of -inf or NaN masks its expert: its score is 0, whatever its bias, and it is chosen only
+ * where a token has fewer than K others, the lowest index first, with weight 0 (all weights are 0 for a
+ * token without any); a group's score leaves it out, and is -inf if nothing else is there.  A bias of
+ * -inf or NaN does the same to the choice.  A logit of +inf counts as the largest fp32 number.
+ *   logits    device fp32 (dtype MOONEP_F32) or bf16 (MOONEP_BF16) [T, E]
+ *   bias      device fp32 [E] or NULL: moves the choice, not the weights
+ *   score     MOONEP_SCORE_*          scale  finite
+ *   topk_ids  device int32 [T, K]     topk_w  device fp32 [T, K]
+ * 1 <= K <= E, E % groups == 0, 1 <= top_groups <= groups, top_groups * (E / groups) >= K; E, K and groups at
+ * most MOONEP_MAX_E, MOONEP_MAX_K and MOONEP_MAX_GROUPS; pointers aligned to their elements.  Outputs must not overlap
+ * anything else (EINVAL).  Deterministic. */
+int moonep_router(const void* logits, int dtype, const float* bias, int64_t T, int E, int K, int score, int groups,
+                  int top_groups, int normalize, float scale, int32_t* topk_ids, float* topk_w, hipStream_t stream);
+
+/* Backward of the router: the logits' gradient from that of the weights (moonep_combine_bwd's dw), with
+ * the choice held fixed.  With g = scale * g_w and, over a token's K experts, p = s / sum(s):
+ *   normalised   p (g - sum(g p)), for the sigmoid times 1 - s
+ *   else         sigmoid: g s (1 - s);  softmax: s (g - sum(g s)), and -s sum(g s) of the logits not chosen
+ * and zero for the other logits, all in fp32, rounded to the logits' type once.  Masked experts (logits of -inf or
+ * NaN) have a gradient of zero; an id outside [0, E) brings nothing; one named twice brings both.
+ *   g_w       device fp32 [T, K]      g_logits  device [T, E], of the logits' type
+ * The other arguments, and errors, as in moonep_router.  Deterministic. */
+int moonep_router_bwd(const void* logits, int dtype, const int32_t* topk_ids, const float* g_w, int64_t T, int E,
+                      int K, int score, int normalize, float scale, void* g_logits, hipStream_t stream);
 
 /* Waits for `stream`, then copies the plan's statistics to the host.  The only call
  * that synchronises: the hot path itself never reads the plan back ("MoonshotAI/MoonEP
