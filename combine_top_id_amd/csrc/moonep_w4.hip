@@ -125,6 +125,7 @@ __device__ __forceinline__ u32x4 expand(uint32_t codes, float scale) {
   return u32x4{codes, 0, 0, (uint32_t)scale};
 #endif
 }
+// Strip t's scale of a word of four, as a float.
 __device__ __forceinline__ float strip_scale(uint32_t scales, int t) {
   return __uint_as_float(t < 3 ? scales << (23 - 8 * t) & 0x7F800000u : scales >> 1 & 0x7F800000u);
 }
@@ -184,26 +185,27 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // A lane's results of a quad's four strips, of one buffer row: gate, gate, up, up, or four of y.  `c` is the
-// lane's place among the quad's columns.
+// lane's place among the quad's columns; `out` and `gu` begin at the tile's first row, `r` is the row of the
+// tile, and what is not `in` goes nowhere.  No branches: every store goes out (see Pipe).
 template <int OP, bool Q8>
-__device__ __forceinline__ void put(const W4Args& a, const f32x4& d, int64_t row, bool in, int quad, int c) {
+__device__ __forceinline__ void put(const W4Args& a, const Window& out, const Window& gu, const f32x4& d, int r, bool in,
+                                    int quad, int c) {
 #ifdef __HIP_DEVICE_COMPILE__
+  const uint32_t at = r * (int)a.out_row;
   if constexpr (OP == W4_FWD2) {
     const int col = quad * kQuadH + 4 * c;
-    if (in && col < a.H)
-      *reinterpret_cast<u32x2*>(a.out + row * a.out_row + col * 2) = u32x2{bf2(d[0], d[1]), bf2(d[2], d[3])};
+    out.store(u32x2{bf2(d[0], d[1]), bf2(d[2], d[3])}, in && col < a.H ? at + col * 2 : kOob);
   } else {
     const int col = quad * kQuadI + 2 * c;
     float slope;
     const float h0 = act_of(d[0], a.act, &slope) * d[2], h1 = act_of(d[1], a.act, &slope) * d[3];
     if constexpr (!Q8) {
-      if (in && col < a.I) {
-        *reinterpret_cast<uint32_t*>(a.out + row * a.out_row + col * 2) = bf2(h0, h1);
-        if (a.gu) {
-          uint16_t* gu = a.gu + row * 2 * a.I + col;
-          *reinterpret_cast<uint32_t*>(gu) = bf2(d[0], d[1]);
-          *reinterpret_cast<uint32_t*>(gu + a.I) = bf2(d[2], d[3]);
-        }
+      in = in && col < a.I;
+      out.store(bf2(h0, h1), in ? at + col * 2 : kOob);
+      if (a.gu) {
+        const uint32_t to = (r * 2 * a.I + col) * 2;
+        gu.store(bf2(d[0], d[1]), in ? to : kOob);
+        gu.store(bf2(d[2], d[3]), in ? to + a.I * 2 : kOob);
       }
     } else {
       // the rule of the 8-bit norm: the smallest power of two that brings the largest of the 32 to 448 =
@@ -212,13 +214,12 @@ __device__ __forceinline__ void put(const W4Args& a, const f32x4& d, int64_t row
       const int ex = max((int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u), 0);
       const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
       const int codes = __builtin_amdgcn_cvt_pk_fp8_f32(h0 * inv, h1 * inv, 0, false);
-      if (in) {
-        uint8_t* p = a.out + row * a.out_row;
-        *reinterpret_cast<uint16_t*>(p + col) = (uint16_t)codes;
-        if (c == 0) p[a.I + quad] = (uint8_t)ex;
-        const int end = a.I + a.I / 32;          // codes, scales, then zeros
-        if (quad == a.I / 32 - 1 && end + c < a.out_row) p[end + c] = 0;
-      }
+      in = in && col < a.I;
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)codes, out.rs, in ? at + col : kOob, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)ex, out.rs, in && c == 0 ? at + a.I + quad : kOob, 0, 0);
+      const int end = a.I + a.I / 32;          // codes, scales, then zeros
+      if (quad == a.I / 32 - 1 && end < a.out_row)
+        __builtin_amdgcn_raw_buffer_store_b8(0, out.rs, in && end + c < a.out_row ? at + end + c : kOob, 0, 0);
     }
   }
 #endif
@@ -311,6 +312,7 @@ __global__ __launch_bounds__(256) void stream_kernel(const W4Args a) {
         load(d, j0 + 4 * (d + D));
       }
     }
+    const Window out(a.out + t.row * a.out_row), gu(a.gu + (int64_t)t.row * 2 * a.I);
     // wave w finishes the rows whose results are the lanes' elements w
 #pragma unroll
     for (int f = 0; f < 4; ++f)
@@ -327,15 +329,310 @@ __global__ __launch_bounds__(256) void stream_kernel(const W4Args a) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) d[f] += part[w][(q * 4 + wave) * 4 + f][lane];
       const int r = q * 16 + g * 4 + wave;
-      put<OP, Q8>(a, d, t.row + r, r < t.rows, t.tn, c);
+      put<OP, Q8>(a, out, gu, d, r, r < t.rows, t.tn, c);
     }
     __syncthreads();
   }
 #endif
 }
 
+// ---------------------------------------------------------------------------------------
+// many rows: tiles of BP rows of weights and BQ buffer rows
+// ---------------------------------------------------------------------------------------
+
+// 4 bytes a lane from the buffer straight into LDS, to `to` + lane * 4 (see load_lds).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(to), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// The products of one tile after another, without a break between them.  LDS holds NB steps of 128 k:
+// the blocks of the tile's quads as they are in memory (a wave's load fills 1024 bytes in the order in
+// which its lanes read them back), and the buffer rows in lines of 128 bytes, 16-byte chunk c of row r
+// in the place of chunk c ^ (r & 7), so that the 16 lanes that read at once hit different banks.
+//
+// A wave multiplies one quad by QF fragments of 16 rows.  A step is cut into parts; in each, the operands
+// of a later part are read from LDS into registers among its matrix instructions.  When all of a step has
+// been read, every wave waits for the next step's loads and for the others, and starts the loads of
+// the step NB further on over it.  One barrier a step.
+template <bool Q8, class G>
+struct W4Pipe {
+  static constexpr int QF = G::QF, NB = G::NB, NW = G::NW, BQ = G::BQ;
+  static constexpr int kLines = Q8 ? 1 : 2;                          // of 128 bytes of a row
+  static constexpr int kP = G::BP / 64 * kBlock, kQ = kLines * BQ * 128, kQS = Q8 ? (BQ > 64 ? BQ : 64) * 4 : 0;
+  static constexpr int kStage = kP + kQ + kQS, kLds = NB * kStage;
+  static constexpr int kLP = G::BP / 16 / NW, kLQ = kQ / 1024 / NW;
+  static constexpr int kLS = Q8 && NW == 4 ? 2 : 1;                  // scales: a wave's loads of 256 bytes
+  static constexpr int kL = kLP + kLQ + kLS;
+  static constexpr int kAhead = (NB - 2) * kL;                       // loads after the next step's
+  static_assert(G::PF == 4 && (NW == 4 || NW == 8) && G::WP == G::BP / 64 && G::BP == 256 && kLP * NW * 16 == G::BP &&
+                kLQ * NW * 1024 == kQ && kLds <= 160 * 1024 && (NB - 1) * kL < 64);
+  uint32_t lds;                   // LDS
+  int wave, lane;
+  int lane_p, lane_q;             // this lane's first LDS byte of a fragment
+  int cur;                        // the current step's place in LDS
+  uint32_t voff_p[kLP], voff_q[kLQ], voff_s, voff_qs;
+  int kc[kLQ];                    // byte of a step that this lane's loads of rows begin with
+  const char *at_p, *at_q, *at_s; // the next step to load
+  int left, todo;                 // bytes of a row left from there, and steps of this tile
+  int loading;                    // its place in LDS
+
+  __device__ __forceinline__ W4Pipe(char* smem, int wave, int lane)
+      : lds((uint32_t)(uintptr_t)(LDS char*)smem), wave(wave), lane(lane), cur(0), loading(0) {
+    const int at = (int)lds, c = lane & 15, g = lane >> 4;
+    lane_p = at + wave % G::WP * kBlock + lane * 16;
+    const int row = wave / G::WP * QF * 16 + c;
+    lane_q = at + kP + (Q8 ? 0 : (g >> 1) * BQ * 128) + row * 128 + (((Q8 ? g : 4 * (g & 1)) ^ (row & 7)) << 4);
+  }
+
+  // The loads of a tile: `w` its first quad's blocks, `nquads` that there are, `nk` blocks to each; `x` its first
+  // row, `rows` rows of `row_bytes`, `kbytes` of them codes or elements.
+  __device__ __forceinline__ void start(const uint8_t* w, int nquads, int nk, const uint8_t* x, int rows, int row_bytes,
+                                        int kbytes, int steps) {
+    const int ln = here(lane);
+    at_p = reinterpret_cast<const char*>(w);
+    at_q = reinterpret_cast<const char*>(x);
+    at_s = at_q + kbytes;
+    left = kbytes;
+    todo = steps;
+#pragma unroll
+    for (int i = 0; i < kLP; ++i) {
+      const int ch = i * NW + wave, quad = ch >> 2;
+      voff_p[i] = quad < nquads ? (uint32_t)(quad * nk * kBlock + (ch & 3) * 1024 + ln * 16) : kOob;
+    }
+#pragma unroll
+    for (int i = 0; i < kLQ; ++i) {
+      const int u = i * NW + wave, line = u / (BQ / 8), r = u % (BQ / 8) * 8 + (ln >> 3);
+      kc[i] = line * 128 + ((ln & 7) ^ (r & 7)) * 16;
+      voff_q[i] = r < rows ? (uint32_t)(r * row_bytes + kc[i]) : kOob;
+    }
+    const int quad = wave & 3, r = scale_rows() * 64 + ln;
+    voff_s = quad < nquads ? (uint32_t)(quad * nk * kBlock + 4096 + ln * 4) : kOob;
+    if (Q8) voff_qs = r < rows && r < BQ ? (uint32_t)(r * row_bytes) : kOob;
+  }
+  // which 64 rows' scales this wave loads
+  __device__ __forceinline__ int scale_rows() const { return (wave & 3) % (BQ >= 64 ? BQ / 64 : 1); }
+
+  // The loads of the next step.  Past the end everything is out of range, and zeros are loaded.
+  template <class F>
+  __device__ __forceinline__ void load(F more) {
+    more();
+    const uint64_t p = reinterpret_cast<uint64_t>(at_p), q = reinterpret_cast<uint64_t>(at_q), s = reinterpret_cast<uint64_t>(at_s);
+    const int range = left > 0 ? 0x7fffffff : 0;
+    const i32x4 rp{(int)p, (int)(p >> 32) & 0xFFFF, range, kBufferFlags}, rq{(int)q, (int)(q >> 32) & 0xFFFF, range, kBufferFlags};
+    if (left < kLines * 128) {                // the last k
+#pragma unroll
+      for (int i = 0; i < kLQ; ++i) voff_q[i] |= kc[i] >= left ? kOob : 0;
+    }
+    const uint32_t to = uni(lds + loading);
+    const uint32_t to_p = uni(to + (wave >> 2) * kBlock + (wave & 3) * 1024), to_q = uni(to + kP + wave * 1024);
+    times<kLP>([&](auto i) { load_lds<i * (NW / 4) * kBlock>(rp, voff_p[i], to_p); });
+    times<kLQ>([&](auto i) { load_lds<i * NW * 1024>(rq, voff_q[i], to_q); });
+    const uint32_t to_s = uni(to + (wave & 3) * kBlock + 4096);
+    if constexpr (!Q8) {
+      load_lds4(rp, voff_s, to_s);
+    } else {
+      const i32x4 rs{(int)s, (int)(s >> 32) & 0xFFFF, range, kBufferFlags};
+      const uint32_t to_qs = uni(to + kP + kQ + scale_rows() * 256);
+      if constexpr (NW == 4) {
+        load_lds4(rp, voff_s, to_s);
+        load_lds4(rs, voff_qs, to_qs);
+      } else {                                // four waves the weights', four the rows'
+        const bool mine = wave < 4;
+        const i32x4 r{mine ? rp[0] : rs[0], mine ? rp[1] : rs[1], range, kBufferFlags};
+        load_lds4(r, mine ? voff_s : voff_qs, uni(mine ? to_s : to_qs));
+      }
+    }
+    at_p += kBlock;
+    at_q += kLines * 128;
+    at_s += 4;
+    left -= kLines * 128;
+    --todo;
+    loading = loading == (NB - 1) * kStage ? 0 : loading + kStage;
+  }
+
+  template <class F>
+  __device__ __forceinline__ void begin(F more) {
+    for (int i = 0; i < NB; ++i) load(more);
+    arrive<(NB - 1) * kL>();
+  }
+
+  struct Rows8 { i32x4 lo, hi; int scale; };
+  __device__ __forceinline__ Rows8 rows8(int at, int q) const {
+    const int x = lane_q + at + q * 2048;
+    // the scale of row r's block g: a byte
+    const int s = (int)lds + kP + kQ + at + (wave / G::WP * QF * 16 + q * 16 + (lane & 15)) * 4 + (lane >> 4);
+    return Rows8{*(const LDS i32x4*)x, *(const LDS i32x4*)(x ^ 64), *(const LDS uint8_t*)s};
+  }
+  __device__ __forceinline__ bf16x8 rows16(int at, int q, int i) const {
+    return *(const LDS bf16x8*)(((lane_q + at) ^ (i << 4)) + q * 2048);
+  }
+  __device__ __forceinline__ i32x4 codes(int at, int f) const { return *(const LDS i32x4*)(lane_p + at + f * 1024); }
+  __device__ __forceinline__ uint32_t scales(int at) const {
+    return *(const LDS uint32_t*)((int)lds + at + wave % G::WP * kBlock + 4096 + lane * 4);
+  }
+
+  // Waits for the next step's loads; `younger`: at least STORES stores went out since the last step.
+  template <int STORES>
+  __device__ __forceinline__ void next_step(bool younger) {
+    constexpr int kMore = kAhead + STORES < 63 ? kAhead + STORES : 63;
+    if (younger) arrive<kMore>();
+    else arrive<kAhead>();
+  }
+
+  template <int F>
+  static __device__ __forceinline__ void multiply8(f32x4& acc, const Rows8& x, const i32x4& p, uint32_t scales) {
+    const i32x8 pw = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8 xw = __builtin_shufflevector(x.lo, x.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xw, pw, acc, 0, 4, 0, x.scale, F, (int)scales);
+  }
+
+  // The next `nk` steps.  `live`: how many of the wave's rows there are; where they are not ALL, the matrix
+  // instructions of the rest are left out.
+  template <bool ALL, int STORES, class F>
+  __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF], F more) {
+    if constexpr (Q8) {
+      constexpr int kRing = QF >= 4 ? 4 : 2, kRead = kRing / 2;        // fragments read ahead
+      i32x4 p[4], pn[4];
+      uint32_t ps, psn = 0;
+      Rows8 x[kRing];
+      times<4>([&](auto f) { p[f] = codes(cur, f); });
+      ps = scales(cur);
+      times<kRead>([&](auto q) { x[q] = rows8(cur, q); });
+      for (int i = 0; i < nk; ++i) {
+        const int nxt = cur == (NB - 1) * kStage ? 0 : cur + kStage;
+        times<QF>([&](auto q) {
+          if constexpr (q == QF - kRead) {
+            next_step<STORES>(younger && i == 0);
+            load(more);
+            times<4>([&](auto f) { pn[f] = codes(nxt, f); });
+            psn = scales(nxt);
+          }
+          x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cur : nxt, (q + kRead) % QF);
+          if (ALL || q * 16 < live)
+            times<4>([&](auto f) { multiply8<f>(acc[f][q], x[q % kRing], p[f], ps); });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        times<4>([&](auto f) { p[f] = pn[f]; });
+        ps = psn;
+        cur = nxt;
+      }
+    } else {
+      i32x4 p[4];
+      uint32_t ps;
+      bf16x8 x[2][QF], w[2][4];
+      auto read = [&](int at) {
+        times<4>([&](auto f) { p[f] = codes(at, f); });
+        ps = scales(at);
+      };
+      read(cur);
+      times<QF>([&](auto q) { x[0][q] = rows16(cur, q, 0); });
+      times<4>([&](auto f) { w[0][f] = __builtin_bit_cast(bf16x8, expand(p[f][0], strip_scale(ps, f))); });
+      for (int i = 0; i < nk; ++i) {
+        const int nxt = cur == (NB - 1) * kStage ? 0 : cur + kStage;
+        times<4>([&](auto k) {
+          constexpr int kn = (k + 1) % 4;
+          if constexpr (k == 3) {
+            next_step<STORES>(younger && i == 0);
+            load(more);
+            read(nxt);
+          }
+          times<QF>([&](auto q) { x[(k + 1) % 2][q] = rows16(k == 3 ? nxt : cur, q, kn); });
+          times<QF>([&](auto q) {
+            if (ALL || q * 16 < live)
+              times<4>([&](auto f) {
+                acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k % 2][q], w[k % 2][f], acc[f][q], 0, 0, 0);
+              });
+          });
+          times<4>([&](auto f) { w[(k + 1) % 2][f] = __builtin_bit_cast(bf16x8, expand(p[f][kn], strip_scale(ps, f))); });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        cur = nxt;
+      }
+    }
+  }
+};
+
+template <int OP, bool Q8, class G>
+__global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int BQ = G::BQ, WP = G::WP, QF = G::QF;
+  constexpr int kQuads = G::BP / 64;
+  using Tiles = W4Pipe<Q8, G>;
+  __shared__ __align__(1024) char smem[Tiles::kLds];
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int wp = wave % WP, wq = wave / WP;
+  if (uni(a.plan[a.s.o_hdr + H_STATUS]) != 0) return;
+  const int K = OP == W4_FWD1 ? a.H : a.I;
+  const int steps = steps_of(K), nk = max(steps, G::NB);      // loads are NB steps ahead, in one more tile only
+  const int quads = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
+  RowTiles<BQ> queue(a.plan, a.s, lane, (quads + kQuads - 1) / kQuads, a.tiles_bound);
+  queue.look_up(0, true);
+  Tiles pipe(smem, wave, lane);
+  auto start = [&](const typename RowTiles<BQ>::Tile& t) {
+    const uint8_t* W = t.w < a.s.E ? a.home + t.w * a.pitch : a.slot + (t.w - a.s.E) * a.pitch;
+    if (OP == W4_FWD2) W += gate_up_bytes(a.H, a.I);
+    const int q0 = t.tn * kQuads;
+    pipe.start(W + (int64_t)q0 * steps * kBlock, quads - q0, steps, a.in + t.row * a.in_row, t.rows, (int)a.in_row,
+               Q8 ? K : 2 * K, nk);
+  };
+  auto cur = queue.tile(0), nxt = queue.tile(1);
+  if (!cur.rows) return;
+  auto more = [&] { if (pipe.todo == 0 && nxt.rows) start(nxt); };
+  start(cur);
+  pipe.begin(more);
+  for (int round = 1;; ++round) {
+    f32x4 acc[4][QF];
+    clear(acc);
+    const auto t = cur;
+    const int quad = t.tn * kQuads + wp;
+    const int live = quad < quads ? t.rows - wq * QF * 16 : 0;
+    constexpr int kStores = 4 * QF;
+    if (live >= QF * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc, more);
+    else pipe.template run<false, kStores>(nk, live, round > 1, acc, more);
+    // what the results' places are made of is worked out here, not kept during the products
+    const int ln = here(lane);
+    const Window out(a.out + t.row * a.out_row), gu(a.gu + (int64_t)t.row * 2 * a.I);
+#pragma unroll
+    for (int q = 0; q < QF; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (wq * QF + q) * 16 + (ln >> 4) * 4 + i;
+        put<OP, Q8>(a, out, gu, f32x4{acc[0][q][i], acc[1][q][i], acc[2][q][i], acc[3][q][i]}, r,
+                    r < t.rows && quad < quads, quad, ln & 15);
+      }
+      __builtin_amdgcn_sched_barrier(0);         // or all results are worked on at once, and spill
+    }
+    if (!nxt.rows) break;
+    cur = nxt;
+    nxt = queue.tile(round + 1);
+  }
+  settled();                      // LDS is not given up while loads may still write to it
+#endif
+}
+
+using W4Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU
+using W4Tall = Geometry<256, 128, 4, 2, 3>;
+using W4Medium = Geometry<256, 64, 4, 1, 3>;       // of 4, two where LDS holds them
+using W4Small = Geometry<256, 32, 4, 1, 3>;
+enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_STREAM };
+
+template <int OP, bool Q8, class G>
+hipError_t launch_tiles(W4Args a, int per_cu, hipStream_t st) {
+  constexpr int kQuads = G::BP / 64;
+  const int64_t mt = a.s.A / G::BQ + std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
+  const int quads = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
+  a.tiles_bound = (int)mt;
+  const int grid = (int)std::min<int64_t>((mt * ((quads + kQuads - 1) / kQuads) + 7) / 8 * 8, per_cu * kCus);
+  hipLaunchKernelGGL((tile_kernel<OP, Q8, G>), dim3(grid), dim3(64 * G::NW), 0, st, a);
+  return hipGetLastError();
+}
+
 template <int OP, bool Q8>
-hipError_t launch(W4Args a, hipStream_t st) {
+hipError_t launch_stream(W4Args a, hipStream_t st) {
   constexpr int NQ = 1, BQ = 16 * NQ;
   const int64_t segs = std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
   const int64_t mt = a.s.A / BQ + segs;
@@ -344,6 +641,25 @@ hipError_t launch(W4Args a, hipStream_t st) {
   const int grid = (int)std::min<int64_t>((mt * nt + 7) / 8 * 8, 8 * kCus);
   hipLaunchKernelGGL((stream_kernel<OP, Q8, NQ>), dim3(grid), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+
+// Which tile: by the mean rows of an expert.
+template <int OP, bool Q8>
+W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
+  const double mean = (double)s.A / std::min<int64_t>(s.E, s.A);
+  return mean <= 1 ? W4_STREAM : mean <= 32 ? W4_SMALL : mean <= 48 ? W4_MEDIUM : mean <= 512 || !Q8 ? W4_TALL : W4_LARGE;
+}
+
+template <int OP, bool Q8>
+hipError_t launch(const W4Args& a, hipStream_t st) {
+  switch (w4_tile<OP, Q8>(a.s, a.H, a.I)) {
+    case W4_LARGE:
+      if constexpr (Q8) return launch_tiles<OP, Q8, W4Large>(a, 1, st);
+    case W4_TALL: return launch_tiles<OP, Q8, W4Tall>(a, 1, st);
+    case W4_MEDIUM: return launch_tiles<OP, Q8, W4Medium>(a, Q8 ? 2 : 1, st);
+    case W4_SMALL: return launch_tiles<OP, Q8, W4Small>(a, 2, st);
+    default: return launch_stream<OP, Q8>(a, st);
+  }
 }
 
 int check_w4(int H, int I) {
