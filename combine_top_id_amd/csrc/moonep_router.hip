@@ -15,7 +15,7 @@ namespace moonep {
 namespace {
 
 constexpr int kMaxGroups = MOONEP_MAX_GROUPS;
-constexpr int kWgs = 256 * 4;              // of the forward kernel, at most: what the CUs hold at once
+constexpr int64_t kWgs = 1 << 23;          // of a grid, at most
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -575,7 +575,7 @@ void launch_fwd(const RouterArgs& a, hipStream_t st) {
 template <class T, int SCORE, bool NORM, int L, int V>
 void launch_bwd(const RouterArgs& a, hipStream_t st) {
   constexpr int kTokens = 256 / L;
-  const unsigned grid = (unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens, 1 << 23);
+  const unsigned grid = (unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens, kWgs);
   hipLaunchKernelGGL((router_bwd_kernel<T, SCORE, NORM, L, V>), dim3(grid), dim3(256), 0, st, a);
 }
 
