@@ -127,6 +127,26 @@ inline bool overlap(const Span& a, std::initializer_list<Span> others) {
   return false;
 }
 
+#ifdef __HIPCC__
+// Orders a wave's LDS writes before its reads: no other wave to wait for.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// NT: a stream larger than the last-level cache passes it by.
+template <bool NT, class T>
+__device__ __forceinline__ T load(const T* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  return *p;
+}
+template <bool NT, class T>
+__device__ __forceinline__ void store(T v, T* p) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+#endif
+
 // chunks per map wave and map sub-blocks per histogram wave
 __host__ __device__ inline int map_chunks(const moonep_sizes& s) {
   const int m = s.blk / kMapThreads;

@@ -38,18 +38,6 @@ __device__ __forceinline__ float block_sum(float v, float (*part)[8], int slot) 
   return s;
 }
 
-// NT: a stream larger than the last-level cache passes it by.
-template <bool NT, class T>
-__device__ __forceinline__ T load(const T* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(p);
-  return *p;
-}
-template <bool NT, class T>
-__device__ __forceinline__ void store(T v, T* p) {
-  if constexpr (NT) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
-
 constexpr int kOutBf16 = 0, kOutQ8 = 1;
 constexpr int kThreads = 512;              // of a workgroup, at most
 

@@ -114,12 +114,6 @@ __device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
   return max(min(a, b), min(max(a, b), c));
 }
 
-// LDS of one wave, which its lanes write and then read: no other wave to wait for.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // What the choice goes by: logits alone, scores and biases, or these in groups.
 enum Mode { kPlain, kBiased, kGrouped };
 

@@ -65,51 +65,61 @@ struct BlockAt {
   }
 };
 
-// A wave a block.  A stream: 64 bytes in for 17 out.
+// A wave a block; in memory's order of the matrix, lane (i, j) of load u has chunk j (8 elements) of row 4 u + i of a
+// strip, so that 16 lanes read 256 bytes that follow each other; the codes get into the slab's order in LDS.  Streams: 64
+// bytes in for 17 out, and back.
+// Measured on MI355X, 16 experts of H 7168, I 2048 (1.4 GB of bf16): with the lanes in the slab's order, whose 16-byte
+// accesses are 64 bytes apart, 375 us and, back, 561; in memory's order 361 and 325, and, where more than the last-level
+// cache holds passes it by, together 651 for 686 (0.2 GB: 39, and 56 if that passed it by).
+template <bool NT>
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* w, int64_t W_el, int64_t n, int H, int I,
                                                    uint8_t* out, int64_t pitch, int64_t per) {
 #ifdef __HIP_DEVICE_COMPILE__   // gfx950 builtins: the host pass needs the kernel's name only
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  __shared__ __align__(16) uint8_t block[4][kBlock];
+  const int lane = threadIdx.x & 63, j = lane & 15, sub = lane >> 4;
+  uint8_t* const mine = block[threadIdx.x >> 6];
   const int64_t all = n * per;
   for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < all; i += (int64_t)gridDim.x * 4) {
     const int64_t e = i / per, b = i - e * per;
     const BlockAt at(b, H, I);
-    const int k = at.k0 + 32 * g;
+    const int k = at.k0 + 8 * j;
     u32x4 v[4][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t row = at.row(t, r);
-      const uint16_t* p = w + e * W_el + at.at + row * at.k + k;
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        v[t][c] = row >= 0 && k + 8 * c < at.k ? *reinterpret_cast<const u32x4*>(p + 8 * c) : u32x4{0, 0, 0, 0};
-    }
-    uint8_t* const to = out + e * pitch + b * kBlock;
-    uint32_t scales = 0;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      uint32_t top = 0;                          // bf16 magnitudes compare as their bits do
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) top = max(top, max(v[t][c][d] & 0x7FFFu, v[t][c][d] >> 16 & 0x7FFFu));
-      // largest = m * 2^E, 1 <= m < 2, and 6 = 1.5 * 2^2; infinities and NaN make the group NaN
-      const int ex = top >= 0x7F80u ? 255 : max((int)(top >> 7) - 2 + ((top & 0x7Fu) > 0x40u), 1);
-      const float scale = __uint_as_float((uint32_t)ex << 23);
-      scales |= (uint32_t)ex << (8 * t);
-      u32x4 codes;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t d = 0;
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][c][0]), hi(v[t][c][0]), scale, 0);
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][c][1]), hi(v[t][c][1]), scale, 1);
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][c][2]), hi(v[t][c][2]), scale, 2);
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][c][3]), hi(v[t][c][3]), scale, 3);
-        codes[c] = d;
+      for (int u = 0; u < 4; ++u) {
+        const int64_t row = at.row(t, 4 * u + sub);
+        v[t][u] = row >= 0 && k < at.k ? load<NT>(reinterpret_cast<const u32x4*>(w + e * W_el + at.at + row * at.k + k))
+                                       : u32x4{0, 0, 0, 0};
       }
-      *reinterpret_cast<u32x4*>(to + t * 1024 + lane * 16) = codes;
-    }
-    *reinterpret_cast<uint32_t*>(to + 4096 + lane * 4) = scales;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t top = 0;                        // bf16 magnitudes compare as their bits do
+#pragma unroll
+        for (int d = 0; d < 4; ++d) top = max(top, max(v[t][u][d] & 0x7FFFu, v[t][u][d] >> 16 & 0x7FFFu));
+        top = max(top, __float_as_uint(quad_move<0xB1>(__uint_as_float(top))));      // four lanes are a group
+        top = max(top, __float_as_uint(quad_move<0x4E>(__uint_as_float(top))));
+        // largest = m * 2^E, 1 <= m < 2, and 6 = 1.5 * 2^2; infinities and NaN make the group NaN
+        const int ex = top >= 0x7F80u ? 255 : max((int)(top >> 7) - 2 + ((top & 0x7Fu) > 0x40u), 1);
+        const float scale = __uint_as_float((uint32_t)ex << 23);
+        uint32_t d = 0;
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][u][0]), hi(v[t][u][0]), scale, 0);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][u][1]), hi(v[t][u][1]), scale, 1);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][u][2]), hi(v[t][u][2]), scale, 2);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, lo(v[t][u][3]), hi(v[t][u][3]), scale, 3);
+        const int to = (j >> 2) * 16 + 4 * u + sub;                  // the lane of the slab's order
+        *reinterpret_cast<uint32_t*>(mine + t * 1024 + to * 16 + (j & 3) * 4) = d;
+        if ((j & 3) == 0) mine[4096 + to * 4 + t] = (uint8_t)ex;
+      }
+    wave_sync();
+    uint8_t* const to = out + e * pitch + b * kBlock;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      store<NT>(*reinterpret_cast<const u32x4*>(mine + t * 1024 + lane * 16), reinterpret_cast<u32x4*>(to + t * 1024 + lane * 16));
+    *reinterpret_cast<uint32_t*>(to + 4096 + lane * 4) = *reinterpret_cast<const uint32_t*>(mine + 4096 + lane * 4);
+    wave_sync();
   }
 #endif
 }
@@ -130,29 +140,33 @@ __device__ __forceinline__ float strip_scale(uint32_t scales, int t) {
   return __uint_as_float(t < 3 ? scales << (23 - 8 * t) & 0x7F800000u : scales >> 1 & 0x7F800000u);
 }
 
-// pack_kernel's inverse, exact.
+// pack_kernel's inverse, exact.  A word of codes comes to the lane that writes its eight elements.
+template <bool NT>
 __global__ __launch_bounds__(256) void unpack_w4_kernel(const uint8_t* in, int64_t pitch, int64_t n, int H, int I,
                                                         uint16_t* w, int64_t W_el, int64_t per) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, j = lane & 15, sub = lane >> 4;
   const int64_t all = n * per;
   for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < all; i += (int64_t)gridDim.x * 4) {
     const int64_t e = i / per, b = i - e * per;
     const BlockAt at(b, H, I);
-    const int k = at.k0 + 32 * g;
+    const int k = at.k0 + 8 * j;
     const uint8_t* from = in + e * pitch + b * kBlock;
-    u32x4 codes[4];
+    uint32_t codes[4][4], scales[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) codes[t] = *reinterpret_cast<const u32x4*>(from + t * 1024 + lane * 16);
-    const uint32_t scales = *reinterpret_cast<const uint32_t*>(from + 4096 + lane * 4);
+    for (int u = 0; u < 4; ++u) {
+      const int l = (j >> 2) * 16 + 4 * u + sub;                     // the lane of the slab's order
+      scales[u] = *reinterpret_cast<const uint32_t*>(from + 4096 + l * 4);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t row = at.row(t, r);
-      if (row < 0) continue;
-      uint16_t* p = w + e * W_el + at.at + row * at.k + k;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (k + 8 * c < at.k) *reinterpret_cast<u32x4*>(p + 8 * c) = expand(codes[t][c], strip_scale(scales, t));
+      for (int t = 0; t < 4; ++t) codes[t][u] = *reinterpret_cast<const uint32_t*>(from + t * 1024 + l * 16 + (j & 3) * 4);
     }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t row = at.row(t, 4 * u + sub);
+        if (row >= 0 && k < at.k)
+          store<NT>(expand(codes[t][u], strip_scale(scales[u], t)), reinterpret_cast<u32x4*>(w + e * W_el + at.at + row * at.k + k));
+      }
   }
 }
 
@@ -682,6 +696,7 @@ int check_packing(const uint16_t* w, int64_t W_el, int64_t n, int H, int I, cons
 
 // Workgroups of four waves, a block to each.
 unsigned pack_grid(int64_t blocks) { return (unsigned)std::min<int64_t>((blocks + 3) / 4, 1 << 23); }
+bool passes_cache(int64_t n, int H, int I) { return n * 6 * I * H > kLastLevelCacheBytes; }
 
 template <bool Q8>
 int ffn_w4(const moonep_plan_desc* plan, const uint8_t* in, int64_t in_row, int H, int I, int act, const uint8_t* home,
@@ -730,7 +745,9 @@ int moonep_w4_pack(const uint16_t* w, int64_t W_el, int64_t n, int H, int I, uin
   if (rc != MOONEP_OK || n == 0) return rc;
   const int64_t per = slab_bytes(H, I) / kBlock;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(pack_kernel, dim3(pack_grid(n * per)), dim3(256), 0, stream, w, W_el, n, H, I, w4, W_bytes, per);
+  const bool nt = passes_cache(n, H, I);
+  hipLaunchKernelGGL((nt ? pack_kernel<true> : pack_kernel<false>), dim3(pack_grid(n * per)), dim3(256), 0, stream, w, W_el, n, H, I, w4,
+                     W_bytes, per);
   return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
@@ -740,7 +757,9 @@ int moonep_w4_unpack(const uint8_t* w4, int64_t W_bytes, int64_t n, int H, int I
   if (rc != MOONEP_OK || n == 0) return rc;
   const int64_t per = slab_bytes(H, I) / kBlock;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(unpack_w4_kernel, dim3(pack_grid(n * per)), dim3(256), 0, stream, w4, W_bytes, n, H, I, w, W_el, per);
+  const bool nt = passes_cache(n, H, I);
+  hipLaunchKernelGGL((nt ? unpack_w4_kernel<true> : unpack_w4_kernel<false>), dim3(pack_grid(n * per)), dim3(256), 0, stream, w4, W_bytes,
+                     n, H, I, w, W_el, per);
   return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_EHIP;
 }
 
