@@ -239,121 +239,6 @@ __device__ __forceinline__ void put(const W4Args& a, const Window& out, const Wi
 #endif
 }
 
-// Few rows: the weights' stream.  A workgroup takes a quad of one row tile; its four waves take the steps
-// along k in turn, each loading its blocks straight into the registers that the matrix instructions
-// take, D steps ahead, and their sums meet in LDS.
-template <int OP, bool Q8, int NQ>
-__global__ __launch_bounds__(256) void stream_kernel(const W4Args a) {
-#ifdef __HIP_DEVICE_COMPILE__
-  constexpr int BQ = 16 * NQ, D = 3;
-  __shared__ float part[4][16 * NQ][64];
-  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-  const int c = lane & 15, g = lane >> 4;
-  if (uni(a.plan[a.s.o_hdr + H_STATUS]) != 0) return;
-  const int K = OP == W4_FWD1 ? a.H : a.I;
-  const int nk = steps_of(K);
-  const int nt = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
-  RowTiles<BQ> queue(a.plan, a.s, lane, nt, a.tiles_bound);
-  queue.look_up(0, true);
-  for (int round = 0;; ++round) {
-    const auto t = queue.tile(round);
-    if (!t.rows) break;
-    const uint8_t* W = t.w < a.s.E ? a.home + t.w * a.pitch : a.slot + (t.w - a.s.E) * a.pitch;
-    if (OP == W4_FWD2) W += gate_up_bytes(a.H, a.I);
-    const auto wr = __builtin_amdgcn_make_buffer_rsrc((void*)(W + (int64_t)t.tn * nk * kBlock), 0, nk * kBlock, kBufferFlags);
-    const auto xr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.in + t.row * a.in_row), 0, 0x7fffffff, kBufferFlags);
-    u32x4 P[D][4], X[D][NQ][Q8 ? 2 : 4];
-    uint32_t S[D], XS[D][NQ];
-    auto load = [&](int d, int j) {               // past the end everything reads as zero
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        P[d][f] = __builtin_amdgcn_raw_buffer_load_b128(wr, j * kBlock + f * 1024 + lane * 16, 0, 0);
-      S[d] = __builtin_amdgcn_raw_buffer_load_b32(wr, j * kBlock + 4096 + lane * 4, 0, 0);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int r = q * 16 + c;
-        const uint32_t row = r < t.rows ? (uint32_t)(r * a.in_row) : kOob;
-        if constexpr (Q8) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int k = j * kStepK + i * 64 + g * 16;
-            X[d][q][i] = __builtin_amdgcn_raw_buffer_load_b128(xr, k < K ? row + k : kOob, 0, 0);
-          }
-          const int b = j * 4 + g;
-          XS[d][q] = __builtin_amdgcn_raw_buffer_load_b8(xr, b * 32 < K ? row + K + b : kOob, 0, 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = j * kStepK + g * 32 + i * 8;
-            X[d][q][i] = __builtin_amdgcn_raw_buffer_load_b128(xr, k < K ? row + k * 2 : kOob, 0, 0);
-          }
-        }
-      }
-    };
-    f32x4 acc[4][NQ];
-    clear(acc);
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(d, wave + 4 * d);
-    for (int j0 = wave; j0 < nk; j0 += 4 * D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          if constexpr (Q8) {
-            const i32x4 pv = __builtin_bit_cast(i32x4, P[d][f]);
-            const i32x8 pw = __builtin_shufflevector(pv, pv, 0, 1, 2, 3, -1, -1, -1, -1);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const i32x8 x = __builtin_shufflevector(__builtin_bit_cast(i32x4, X[d][q][0]),
-                                                      __builtin_bit_cast(i32x4, X[d][q][1]), 0, 1, 2, 3, 4, 5, 6, 7);
-              // the strip's byte of S
-              if (f == 0) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, pw, acc[f][q], 0, 4, 0, XS[d][q], 0, S[d]);
-              if (f == 1) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, pw, acc[f][q], 0, 4, 0, XS[d][q], 1, S[d]);
-              if (f == 2) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, pw, acc[f][q], 0, 4, 0, XS[d][q], 2, S[d]);
-              if (f == 3) acc[f][q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, pw, acc[f][q], 0, 4, 0, XS[d][q], 3, S[d]);
-            }
-          } else {
-            const float scale = strip_scale(S[d], f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bf16x8 p = __builtin_bit_cast(bf16x8, expand(P[d][f][i], scale));
-#pragma unroll
-              for (int q = 0; q < NQ; ++q)
-                acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, X[d][q][i]), p, acc[f][q], 0, 0, 0);
-            }
-          }
-        }
-        load(d, j0 + 4 * (d + D));
-      }
-    }
-    const Window out(a.out + t.row * a.out_row), gu(a.gu + (int64_t)t.row * 2 * a.I);
-    // wave w finishes the rows whose results are the lanes' elements w
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][(q * 4 + i) * 4 + f][lane] = acc[f][q][i];
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      f32x4 d{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) d[f] += part[w][(q * 4 + wave) * 4 + f][lane];
-      const int r = q * 16 + g * 4 + wave;
-      put<OP, Q8>(a, out, gu, d, r, r < t.rows, t.tn, c);
-    }
-    __syncthreads();
-  }
-#endif
-}
-
-// ---------------------------------------------------------------------------------------
-// many rows: tiles of BP rows of weights and BQ buffer rows
-// ---------------------------------------------------------------------------------------
-
 // 4 bytes a lane from the buffer straight into LDS, to `to` + lane * 4 (see load_lds).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
@@ -363,139 +248,161 @@ __device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t to
 }
 #pragma clang diagnostic pop
 
-// The products of one tile after another, without a break between them.  LDS holds NB steps of 128 k:
-// the blocks of the tile's quads as they are in memory (a wave's load fills 1024 bytes in the order in
-// which its lanes read them back), and the buffer rows in lines of 128 bytes, 16-byte chunk c of row r
+// A tile of BP x BQ results by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
+// of weights and NQ of rows.
+template <int WP_, int BQ_, int WQ_, int NP_, int NQ_>
+struct W4Geometry {
+  static constexpr int WP = WP_, WQ = WQ_, NW = WP * WQ, BP = 64 * WP, BQ = BQ_, QF = BQ / WQ / 16, NP = NP_, NQ = NQ_;
+};
+
+// The products of one tile after another, without a break between them.  LDS holds NP steps of 128 k of weights, the
+// blocks of the tile's quads as they are in memory (a wave's load fills 1024 bytes in the order in
+// which its lanes read them back), and NQ steps of the buffer rows, in lines of 128 bytes, 16-byte chunk c of row r
 // in the place of chunk c ^ (r & 7), so that the 16 lanes that read at once hit different banks.
 //
-// A wave multiplies one quad by QF fragments of 16 rows.  A step is cut into parts; in each, the operands
-// of a later part are read from LDS into registers among its matrix instructions.  When all of a step has
-// been read, every wave waits for the next step's loads and for the others, and starts the loads of
-// the step NB further on over it.  One barrier a step.
+// The first half of the waves loads the weights, the other the rows: loads are waited for in their order, so a
+// wave that loaded both could have no more weights on their way than rows.
+//
+// A step is cut into parts; in each, the operands of a later part are read from LDS into registers among its matrix
+// instructions.  When all of a step has been read, every wave waits for the next step's loads and for the others, and
+// starts the loads of the step NP (or NQ) further on over it.  One barrier a step.
 template <bool Q8, class G>
 struct W4Pipe {
-  static constexpr int QF = G::QF, NB = G::NB, NW = G::NW, BQ = G::BQ;
+  static constexpr int QF = G::QF, NW = G::NW, BQ = G::BQ, WP = G::WP, NP = G::NP, NQ = G::NQ;
   static constexpr int kLines = Q8 ? 1 : 2;                          // of 128 bytes of a row
-  static constexpr int kP = G::BP / 64 * kBlock, kQ = kLines * BQ * 128, kQS = Q8 ? (BQ > 64 ? BQ : 64) * 4 : 0;
-  static constexpr int kStage = kP + kQ + kQS, kLds = NB * kStage;
-  static constexpr int kLP = G::BP / 16 / NW, kLQ = kQ / 1024 / NW;
-  static constexpr int kLS = Q8 && NW == 4 ? 2 : 1;                  // scales: a wave's loads of 256 bytes
-  static constexpr int kL = kLP + kLQ + kLS;
-  static constexpr int kAhead = (NB - 2) * kL;                       // loads after the next step's
-  static_assert(G::PF == 4 && (NW == 4 || NW == 8) && G::WP == G::BP / 64 && G::BP == 256 && kLP * NW * 16 == G::BP &&
-                kLQ * NW * 1024 == kQ && kLds <= 160 * 1024 && (NB - 1) * kL < 64);
+  static constexpr int kHalf = NW / 2;                               // waves that load one side
+  static constexpr int kRW = BQ / kHalf;                             // rows whose scales a wave loads
+  static constexpr int kP = WP * kBlock, kQB = kLines * BQ * 128, kQ = kQB + (Q8 ? kHalf * 256 : 0);
+  static constexpr int kQ0 = NP * kP, kLds = NP * kP + NQ * kQ;
+  static constexpr int kCP = WP * 4 / kHalf, kSP = WP / kHalf, kLP = kCP + kSP;      // a wave's loads of a step
+  static constexpr int kCQ = kQB / 1024 / kHalf, kLQ = kCQ + (Q8 ? 1 : 0);
+  static_assert(kHalf >= 1 && kCP * kHalf == WP * 4 && kSP * kHalf == WP && kCQ * kHalf * 1024 == kQB && kRW <= 64 &&
+                kLds <= 160 * 1024 && NP >= 2 && NQ >= 2 && (NP - 1) * kLP < 48 && (NQ - 1) * kLQ < 48);
+  static constexpr int kSteps = NP > NQ ? NP : NQ;                   // loads are that far ahead
   uint32_t lds;                   // LDS
   int wave, lane;
-  int lane_p, lane_q;             // this lane's first LDS byte of a fragment
-  int cur;                        // the current step's place in LDS
-  uint32_t voff_p[kLP], voff_q[kLQ], voff_s, voff_qs;
-  int kc[kLQ];                    // byte of a step that this lane's loads of rows begin with
-  const char *at_p, *at_q, *at_s; // the next step to load
+  bool rows;                      // this wave loads rows (uniform)
+  int lane_p, lane_q, lane_s;     // this lane's first LDS byte of a fragment of weights, of rows, of a row's scale
+  int cp, cq;                     // the current step's places in LDS
+  uint32_t voff, voff_s;          // this lane's first load and its scale's
+  uint32_t stride;                // bytes from a quad to the next, or of kHalf * 8 rows (uniform)
+  const char *at, *at_s;          // the next step to load
+  int range;                      // bytes from there to the tile's end: what is past it reads as zero
   int left, todo;                 // bytes of a row left from there, and steps of this tile
   int loading;                    // its place in LDS
 
   __device__ __forceinline__ W4Pipe(char* smem, int wave, int lane)
-      : lds((uint32_t)(uintptr_t)(LDS char*)smem), wave(wave), lane(lane), cur(0), loading(0) {
-    const int at = (int)lds, c = lane & 15, g = lane >> 4;
-    lane_p = at + wave % G::WP * kBlock + lane * 16;
-    const int row = wave / G::WP * QF * 16 + c;
-    lane_q = at + kP + (Q8 ? 0 : (g >> 1) * BQ * 128) + row * 128 + (((Q8 ? g : 4 * (g & 1)) ^ (row & 7)) << 4);
+      : lds((uint32_t)(uintptr_t)(LDS char*)smem), wave(wave), lane(lane), rows(wave >= kHalf), cp(0), cq(kQ0) {
+    const int base = (int)lds, c = lane & 15, g = lane >> 4;
+    loading = rows ? kQ0 : 0;
+    lane_p = base + wave % WP * kBlock + lane * 16;
+    const int row = wave / WP * QF * 16 + c;
+    lane_q = base + (Q8 ? 0 : (g >> 1) * BQ * 128) + row * 128 + (((Q8 ? g : 4 * (g & 1)) ^ (row & 7)) << 4);
+    lane_s = base + kQB + scale_at(row) + g;
   }
+  static __device__ __forceinline__ int scale_at(int row) { return row / kRW * 256 + row % kRW * 4; }
 
   // The loads of a tile: `w` its first quad's blocks, `nquads` that there are, `nk` blocks to each; `x` its first
-  // row, `rows` rows of `row_bytes`, `kbytes` of them codes or elements.
-  __device__ __forceinline__ void start(const uint8_t* w, int nquads, int nk, const uint8_t* x, int rows, int row_bytes,
+  // row, `n` rows of `row_bytes`, `kbytes` of them codes or elements.
+  __device__ __forceinline__ void start(const uint8_t* w, int nquads, int nk, const uint8_t* x, int n, int row_bytes,
                                         int kbytes, int steps) {
     const int ln = here(lane);
-    at_p = reinterpret_cast<const char*>(w);
-    at_q = reinterpret_cast<const char*>(x);
-    at_s = at_q + kbytes;
     left = kbytes;
     todo = steps;
-#pragma unroll
-    for (int i = 0; i < kLP; ++i) {
-      const int ch = i * NW + wave, quad = ch >> 2;
-      voff_p[i] = quad < nquads ? (uint32_t)(quad * nk * kBlock + (ch & 3) * 1024 + ln * 16) : kOob;
+    if (!rows) {
+      at = reinterpret_cast<const char*>(w);
+      stride = nk * kBlock;
+      range = nquads < WP ? nquads * (int)stride : WP * (int)stride;
+      voff = (wave >> 2) * stride + (wave & 3) * 1024 + ln * 16;
+      voff_s = wave * stride + 4096 + ln * 4;
+    } else {
+      at = reinterpret_cast<const char*>(x);
+      at_s = at + kbytes;
+      stride = kHalf * 8 * row_bytes;
+      range = n * row_bytes;
+      const int r = (wave - kHalf) * 8 + (ln >> 3);
+      voff = r * row_bytes + ((ln & 7) ^ (ln >> 3)) * 16;
+      voff_s = ln < kRW ? (uint32_t)(((wave - kHalf) * kRW + ln) * row_bytes) : kOob;
     }
-#pragma unroll
-    for (int i = 0; i < kLQ; ++i) {
-      const int u = i * NW + wave, line = u / (BQ / 8), r = u % (BQ / 8) * 8 + (ln >> 3);
-      kc[i] = line * 128 + ((ln & 7) ^ (r & 7)) * 16;
-      voff_q[i] = r < rows ? (uint32_t)(r * row_bytes + kc[i]) : kOob;
-    }
-    const int quad = wave & 3, r = scale_rows() * 64 + ln;
-    voff_s = quad < nquads ? (uint32_t)(quad * nk * kBlock + 4096 + ln * 4) : kOob;
-    if (Q8) voff_qs = r < rows && r < BQ ? (uint32_t)(r * row_bytes) : kOob;
   }
-  // which 64 rows' scales this wave loads
-  __device__ __forceinline__ int scale_rows() const { return (wave & 3) % (BQ >= 64 ? BQ / 64 : 1); }
 
   // The loads of the next step.  Past the end everything is out of range, and zeros are loaded.
   template <class F>
   __device__ __forceinline__ void load(F more) {
     more();
-    const uint64_t p = reinterpret_cast<uint64_t>(at_p), q = reinterpret_cast<uint64_t>(at_q), s = reinterpret_cast<uint64_t>(at_s);
-    const int range = left > 0 ? 0x7fffffff : 0;
-    const i32x4 rp{(int)p, (int)(p >> 32) & 0xFFFF, range, kBufferFlags}, rq{(int)q, (int)(q >> 32) & 0xFFFF, range, kBufferFlags};
-    if (left < kLines * 128) {                // the last k
-#pragma unroll
-      for (int i = 0; i < kLQ; ++i) voff_q[i] |= kc[i] >= left ? kOob : 0;
-    }
-    const uint32_t to = uni(lds + loading);
-    const uint32_t to_p = uni(to + (wave >> 2) * kBlock + (wave & 3) * 1024), to_q = uni(to + kP + wave * 1024);
-    times<kLP>([&](auto i) { load_lds<i * (NW / 4) * kBlock>(rp, voff_p[i], to_p); });
-    times<kLQ>([&](auto i) { load_lds<i * NW * 1024>(rq, voff_q[i], to_q); });
-    const uint32_t to_s = uni(to + (wave & 3) * kBlock + 4096);
-    if constexpr (!Q8) {
-      load_lds4(rp, voff_s, to_s);
+    const uint64_t p = reinterpret_cast<uint64_t>(at);
+    const i32x4 rs{(int)p, (int)(p >> 32) & 0xFFFF, left > 0 ? range : 0, kBufferFlags};
+    if (!rows) {
+      // chunk i * kHalf + wave of the step's, strip by strip
+      const uint32_t to = uni(lds + loading + (wave >> 2) * kBlock + (wave & 3) * 1024);
+      times<kCP>([&](auto i) {
+        load_lds<(i * kHalf >> 2) * kBlock + (i * kHalf & 3) * 1024>(rs, voff + (i * kHalf >> 2) * stride + (i * kHalf & 3) * 1024, to);
+      });
+      times<kSP>([&](auto i) {
+        load_lds4(rs, voff_s + i * kHalf * stride, uni(lds + loading + (i * kHalf + wave) * kBlock + 4096));
+      });
+      at += kBlock;
+      range -= kBlock;
+      loading = loading == (NP - 1) * kP ? 0 : loading + kP;
     } else {
-      const i32x4 rs{(int)s, (int)(s >> 32) & 0xFFFF, range, kBufferFlags};
-      const uint32_t to_qs = uni(to + kP + kQ + scale_rows() * 256);
-      if constexpr (NW == 4) {
-        load_lds4(rp, voff_s, to_s);
-        load_lds4(rs, voff_qs, to_qs);
-      } else {                                // four waves the weights', four the rows'
-        const bool mine = wave < 4;
-        const i32x4 r{mine ? rp[0] : rs[0], mine ? rp[1] : rs[1], range, kBufferFlags};
-        load_lds4(r, mine ? voff_s : voff_qs, uni(mine ? to_s : to_qs));
+      const uint32_t to = uni(lds + loading + (wave - kHalf) * 1024);
+      const int c = ((lane & 7) ^ (lane >> 3)) * 16;
+      times<kCQ>([&](auto i) {                // eight rows of a line of 128 bytes
+        constexpr int kLine = i * kHalf / (BQ / 8), kRow = i * kHalf % (BQ / 8) / kHalf;
+        static_assert(BQ / 8 % kHalf == 0);
+        const uint32_t v = voff + kRow * stride + kLine * 128;
+        load_lds<i * kHalf * 1024>(rs, c + kLine * 128 < left ? v : kOob, to);
+      });
+      if constexpr (Q8) {
+        const uint64_t s = reinterpret_cast<uint64_t>(at_s);
+        const i32x4 r{(int)s, (int)(s >> 32) & 0xFFFF, left > 0 ? scale_range() : 0, kBufferFlags};
+        load_lds4(r, voff_s, uni(lds + loading + kQB + (wave - kHalf) * 256));
+        at_s += 4;
       }
+      at += kLines * 128;
+      range -= kLines * 128;
+      loading = loading == kQ0 + (NQ - 1) * kQ ? kQ0 : loading + kQ;
     }
-    at_p += kBlock;
-    at_q += kLines * 128;
-    at_s += 4;
     left -= kLines * 128;
     --todo;
-    loading = loading == (NB - 1) * kStage ? 0 : loading + kStage;
+  }
+  // From a row's scales of the next step to the tile's end, which is that of its last row: left bytes of codes, and
+  // the scales that have been loaded.
+  __device__ __forceinline__ int scale_range() const { return range - (int)(at_s - at); }
+
+  // Waits until at most `steps` steps of this wave's loads are on their way, and, where `younger` is set, the STORES
+  // stores that went out after them.
+  template <int LESS, int STORES>
+  __device__ __forceinline__ void wait(bool younger) {
+    constexpr int kMoreP = (NP - LESS) * kLP + STORES, kMoreQ = (NQ - LESS) * kLQ + STORES;
+    asm volatile("" ::: "memory");
+    if (younger) {
+      if (!rows) __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMoreP < 63 ? kMoreP : 63));
+      else __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMoreQ < 63 ? kMoreQ : 63));
+    } else {
+      if (!rows) __builtin_amdgcn_s_waitcnt(wait_vm_lds((NP - LESS) * kLP));
+      else __builtin_amdgcn_s_waitcnt(wait_vm_lds((NQ - LESS) * kLQ));
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
 
   template <class F>
   __device__ __forceinline__ void begin(F more) {
-    for (int i = 0; i < NB; ++i) load(more);
-    arrive<(NB - 1) * kL>();
+    for (int i = 0; i < (rows ? NQ : NP); ++i) load(more);
+    wait<1, 0>(false);
   }
 
   struct Rows8 { i32x4 lo, hi; int scale; };
   __device__ __forceinline__ Rows8 rows8(int at, int q) const {
     const int x = lane_q + at + q * 2048;
-    // the scale of row r's block g: a byte
-    const int s = (int)lds + kP + kQ + at + (wave / G::WP * QF * 16 + q * 16 + (lane & 15)) * 4 + (lane >> 4);
-    return Rows8{*(const LDS i32x4*)x, *(const LDS i32x4*)(x ^ 64), *(const LDS uint8_t*)s};
+    return Rows8{*(const LDS i32x4*)x, *(const LDS i32x4*)(x ^ 64), *(const LDS uint8_t*)(lane_s + at + (scale_at(q * 16) - scale_at(0)))};
   }
   __device__ __forceinline__ bf16x8 rows16(int at, int q, int i) const {
     return *(const LDS bf16x8*)(((lane_q + at) ^ (i << 4)) + q * 2048);
   }
   __device__ __forceinline__ i32x4 codes(int at, int f) const { return *(const LDS i32x4*)(lane_p + at + f * 1024); }
-  __device__ __forceinline__ uint32_t scales(int at) const {
-    return *(const LDS uint32_t*)((int)lds + at + wave % G::WP * kBlock + 4096 + lane * 4);
-  }
-
-  // Waits for the next step's loads; `younger`: at least STORES stores went out since the last step.
-  template <int STORES>
-  __device__ __forceinline__ void next_step(bool younger) {
-    constexpr int kMore = kAhead + STORES < 63 ? kAhead + STORES : 63;
-    if (younger) arrive<kMore>();
-    else arrive<kAhead>();
-  }
+  __device__ __forceinline__ uint32_t scales(int at) const { return *(const LDS uint32_t*)((lane_p - lane * 12) + at + 4096); }
 
   template <int F>
   static __device__ __forceinline__ void multiply8(f32x4& acc, const Rows8& x, const i32x4& p, uint32_t scales) {
@@ -505,34 +412,37 @@ struct W4Pipe {
   }
 
   // The next `nk` steps.  `live`: how many of the wave's rows there are; where they are not ALL, the matrix
-  // instructions of the rest are left out.
+  // instructions of the rest are left out.  `younger`: at least STORES stores went out since the last step.
   template <bool ALL, int STORES, class F>
   __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF], F more) {
     if constexpr (Q8) {
-      constexpr int kRing = QF >= 4 ? 4 : 2, kRead = kRing / 2;        // fragments read ahead
+      constexpr int kRing = QF >= 4 ? 4 : 2, kRead = QF > 1 ? kRing / 2 : 1;        // fragments read ahead
       i32x4 p[4], pn[4];
       uint32_t ps, psn = 0;
       Rows8 x[kRing];
-      times<4>([&](auto f) { p[f] = codes(cur, f); });
-      ps = scales(cur);
-      times<kRead>([&](auto q) { x[q] = rows8(cur, q); });
+      times<4>([&](auto f) { p[f] = codes(cp, f); });
+      ps = scales(cp);
+      times<kRead>([&](auto q) { x[q] = rows8(cq, q); });
       for (int i = 0; i < nk; ++i) {
-        const int nxt = cur == (NB - 1) * kStage ? 0 : cur + kStage;
+        const int np = cp == (NP - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NQ - 1) * kQ ? kQ0 : cq + kQ;
         times<QF>([&](auto q) {
           if constexpr (q == QF - kRead) {
-            next_step<STORES>(younger && i == 0);
+            wait<2, STORES>(younger && i == 0);
             load(more);
-            times<4>([&](auto f) { pn[f] = codes(nxt, f); });
-            psn = scales(nxt);
+            times<4>([&](auto f) { pn[f] = codes(np, f); });
+            psn = scales(np);
           }
-          x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cur : nxt, (q + kRead) % QF);
+          // QF = 1: the one place is read anew after it has been multiplied
+          if constexpr (QF > 1) x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cq : nq, (q + kRead) % QF);
           if (ALL || q * 16 < live)
             times<4>([&](auto f) { multiply8<f>(acc[f][q], x[q % kRing], p[f], ps); });
+          if constexpr (QF == 1) x[0] = rows8(nq, 0);
           __builtin_amdgcn_sched_barrier(0);
         });
         times<4>([&](auto f) { p[f] = pn[f]; });
         ps = psn;
-        cur = nxt;
+        cp = np;
+        cq = nq;
       }
     } else {
       i32x4 p[4];
@@ -542,19 +452,19 @@ struct W4Pipe {
         times<4>([&](auto f) { p[f] = codes(at, f); });
         ps = scales(at);
       };
-      read(cur);
-      times<QF>([&](auto q) { x[0][q] = rows16(cur, q, 0); });
+      read(cp);
+      times<QF>([&](auto q) { x[0][q] = rows16(cq, q, 0); });
       times<4>([&](auto f) { w[0][f] = __builtin_bit_cast(bf16x8, expand(p[f][0], strip_scale(ps, f))); });
       for (int i = 0; i < nk; ++i) {
-        const int nxt = cur == (NB - 1) * kStage ? 0 : cur + kStage;
+        const int np = cp == (NP - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NQ - 1) * kQ ? kQ0 : cq + kQ;
         times<4>([&](auto k) {
           constexpr int kn = (k + 1) % 4;
           if constexpr (k == 3) {
-            next_step<STORES>(younger && i == 0);
+            wait<2, STORES>(younger && i == 0);
             load(more);
-            read(nxt);
+            read(np);
           }
-          times<QF>([&](auto q) { x[(k + 1) % 2][q] = rows16(k == 3 ? nxt : cur, q, kn); });
+          times<QF>([&](auto q) { x[(k + 1) % 2][q] = rows16(k == 3 ? nq : cq, q, kn); });
           times<QF>([&](auto q) {
             if (ALL || q * 16 < live)
               times<4>([&](auto f) {
@@ -564,7 +474,8 @@ struct W4Pipe {
           times<4>([&](auto f) { w[(k + 1) % 2][f] = __builtin_bit_cast(bf16x8, expand(p[f][kn], strip_scale(ps, f))); });
           __builtin_amdgcn_sched_barrier(0);
         });
-        cur = nxt;
+        cp = np;
+        cq = nq;
       }
     }
   }
@@ -581,7 +492,7 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
   const int wp = wave % WP, wq = wave / WP;
   if (uni(a.plan[a.s.o_hdr + H_STATUS]) != 0) return;
   const int K = OP == W4_FWD1 ? a.H : a.I;
-  const int steps = steps_of(K), nk = max(steps, G::NB);      // loads are NB steps ahead, in one more tile only
+  const int steps = steps_of(K), nk = max(steps, Tiles::kSteps);      // loads are that far ahead, in one more tile only
   const int quads = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
   RowTiles<BQ> queue(a.plan, a.s, lane, (quads + kQuads - 1) / kQuads, a.tiles_bound);
   queue.look_up(0, true);
@@ -628,11 +539,12 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
 #endif
 }
 
-using W4Large = Geometry<256, 256, 4, 2, 3>;       // one workgroup of 8 waves to a CU
-using W4Tall = Geometry<256, 128, 4, 2, 3>;
-using W4Medium = Geometry<256, 64, 4, 1, 3>;       // of 4, two where LDS holds them
-using W4Small = Geometry<256, 32, 4, 1, 3>;
-enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_STREAM };
+using W4Large = W4Geometry<4, 256, 2, 3, 3>;
+using W4Tall = W4Geometry<4, 128, 2, 3, 3>;
+using W4Medium = W4Geometry<4, 64, 1, 3, 3>;
+using W4Small = W4Geometry<4, 32, 1, 3, 3>;
+using W4Few = W4Geometry<2, 16, 1, 4, 2>;          // of 2
+enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_FEW };
 
 template <int OP, bool Q8, class G>
 hipError_t launch_tiles(W4Args a, int per_cu, hipStream_t st) {
@@ -645,23 +557,11 @@ hipError_t launch_tiles(W4Args a, int per_cu, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int OP, bool Q8>
-hipError_t launch_stream(W4Args a, hipStream_t st) {
-  constexpr int NQ = 1, BQ = 16 * NQ;
-  const int64_t segs = std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
-  const int64_t mt = a.s.A / BQ + segs;
-  const int nt = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
-  a.tiles_bound = (int)mt;
-  const int grid = (int)std::min<int64_t>((mt * nt + 7) / 8 * 8, 8 * kCus);
-  hipLaunchKernelGGL((stream_kernel<OP, Q8, NQ>), dim3(grid), dim3(256), 0, st, a);
-  return hipGetLastError();
-}
-
 // Which tile: by the mean rows of an expert.
 template <int OP, bool Q8>
 W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
   const double mean = (double)s.A / std::min<int64_t>(s.E, s.A);
-  return mean <= 1 ? W4_STREAM : mean <= 32 ? W4_SMALL : mean <= 48 ? W4_MEDIUM : mean <= 512 || !Q8 ? W4_TALL : W4_LARGE;
+  return mean <= 12 ? W4_FEW : mean <= 32 ? W4_SMALL : mean <= 48 ? W4_MEDIUM : mean <= 512 || !Q8 ? W4_TALL : W4_LARGE;
 }
 
 template <int OP, bool Q8>
@@ -672,7 +572,7 @@ hipError_t launch(const W4Args& a, hipStream_t st) {
     case W4_TALL: return launch_tiles<OP, Q8, W4Tall>(a, 1, st);
     case W4_MEDIUM: return launch_tiles<OP, Q8, W4Medium>(a, Q8 ? 2 : 1, st);
     case W4_SMALL: return launch_tiles<OP, Q8, W4Small>(a, 2, st);
-    default: return launch_stream<OP, Q8>(a, st);
+    default: return launch_tiles<OP, Q8, W4Few>(a, Q8 ? 4 : 3, st);
   }
 }
 
