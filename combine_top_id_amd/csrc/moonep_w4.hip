@@ -258,7 +258,9 @@ struct W4Geometry {
 // The products of one tile after another, without a break between them.  LDS holds NP steps of 128 k of weights, the
 // blocks of the tile's quads as they are in memory (a wave's load fills 1024 bytes in the order in
 // which its lanes read them back), and NQ steps of the buffer rows, in lines of 128 bytes, 16-byte chunk c of row r
-// in the place of chunk c ^ (r & 7), so that the 16 lanes that read at once hit different banks.
+// in the place of chunk c ^ (r & 7), so that the 16 lanes that read at once hit different banks.  A step's 256 bytes
+// of a bf16 row are two lines: line L has, as chunks 4 j + g, k = 32 g + 16 L + 8 j ... + 7, since a
+// matrix instruction's lanes take neighbours in g.
 //
 // The first half of the waves loads the weights, the other the rows: loads are waited for in their order, so a
 // wave that loaded both could have no more weights on their way than rows.
@@ -290,14 +292,17 @@ struct W4Pipe {
   int range;                      // bytes from there to the tile's end: what is past it reads as zero
   int left, todo;                 // bytes of a row left from there, and steps of this tile
   int loading;                    // its place in LDS
+  int first;                      // the byte of a row's step that this lane loads first
 
   __device__ __forceinline__ W4Pipe(char* smem, int wave, int lane)
       : lds((uint32_t)(uintptr_t)(LDS char*)smem), wave(wave), lane(lane), rows(wave >= kHalf), cp(0), cq(kQ0) {
     const int base = (int)lds, c = lane & 15, g = lane >> 4;
     loading = rows ? kQ0 : 0;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    first = Q8 ? chunk * 16 : (chunk & 3) * 64 + (chunk >> 2) * 16;
     lane_p = base + wave % WP * kBlock + lane * 16;
     const int row = wave / WP * QF * 16 + c;
-    lane_q = base + (Q8 ? 0 : (g >> 1) * BQ * 128) + row * 128 + (((Q8 ? g : 4 * (g & 1)) ^ (row & 7)) << 4);
+    lane_q = base + row * 128 + ((g ^ (row & 7)) << 4);
     lane_s = base + kQB + scale_at(row) + g;
   }
   static __device__ __forceinline__ int scale_at(int row) { return row / kRW * 256 + row % kRW * 4; }
@@ -321,7 +326,7 @@ struct W4Pipe {
       stride = kHalf * 8 * row_bytes;
       range = n * row_bytes;
       const int r = (wave - kHalf) * 8 + (ln >> 3);
-      voff = r * row_bytes + ((ln & 7) ^ (ln >> 3)) * 16;
+      voff = r * row_bytes + first;
       voff_s = ln < kRW ? (uint32_t)(((wave - kHalf) * kRW + ln) * row_bytes) : kOob;
     }
   }
@@ -346,12 +351,12 @@ struct W4Pipe {
       loading = loading == (NP - 1) * kP ? 0 : loading + kP;
     } else {
       const uint32_t to = uni(lds + loading + (wave - kHalf) * 1024);
-      const int c = ((lane & 7) ^ (lane >> 3)) * 16;
       times<kCQ>([&](auto i) {                // eight rows of a line of 128 bytes
         constexpr int kLine = i * kHalf / (BQ / 8), kRow = i * kHalf % (BQ / 8) / kHalf;
         static_assert(BQ / 8 % kHalf == 0);
-        const uint32_t v = voff + kRow * stride + kLine * 128;
-        load_lds<i * kHalf * 1024>(rs, c + kLine * 128 < left ? v : kOob, to);
+        constexpr int kSkip = kLine * (Q8 ? 128 : 32);
+        const uint32_t v = voff + kRow * stride + kSkip;
+        load_lds<i * kHalf * 1024>(rs, first + kSkip < left ? v : kOob, to);
       });
       if constexpr (Q8) {
         const uint64_t s = reinterpret_cast<uint64_t>(at_s);
@@ -395,11 +400,11 @@ struct W4Pipe {
 
   struct Rows8 { i32x4 lo, hi; int scale; };
   __device__ __forceinline__ Rows8 rows8(int at, int q) const {
-    const int x = lane_q + at + q * 2048;
-    return Rows8{*(const LDS i32x4*)x, *(const LDS i32x4*)(x ^ 64), *(const LDS uint8_t*)(lane_s + at + (scale_at(q * 16) - scale_at(0)))};
+    const int x = lane_q + at, y = x ^ 64;
+    return Rows8{*(const LDS i32x4*)(x + q * 2048), *(const LDS i32x4*)(y + q * 2048), *(const LDS uint8_t*)(lane_s + at + (scale_at(q * 16) - scale_at(0)))};
   }
   __device__ __forceinline__ bf16x8 rows16(int at, int q, int i) const {
-    return *(const LDS bf16x8*)(((lane_q + at) ^ (i << 4)) + q * 2048);
+    return *(const LDS bf16x8*)(((lane_q + at) ^ (i & 1) << 6) + (i >> 1) * BQ * 128 + q * 2048);
   }
   __device__ __forceinline__ i32x4 codes(int at, int f) const { return *(const LDS i32x4*)(lane_p + at + f * 1024); }
   __device__ __forceinline__ uint32_t scales(int at) const { return *(const LDS uint32_t*)((lane_p - lane * 12) + at + 4096); }
