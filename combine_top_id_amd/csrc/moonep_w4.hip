@@ -307,34 +307,45 @@ struct W4Pipe {
   }
   static __device__ __forceinline__ int scale_at(int row) { return row / kRW * 256 + row % kRW * 4; }
 
-  // The loads of a tile: `w` its first quad's blocks, `nquads` that there are, `nk` blocks to each; `x` its first
-  // row, `n` rows of `row_bytes`, `kbytes` of them codes or elements.
-  __device__ __forceinline__ void start(const uint8_t* w, int nquads, int nk, const uint8_t* x, int n, int row_bytes,
-                                        int kbytes, int steps) {
-    const int ln = here(lane);
+  // One side of a tile: where it begins, and its bytes (0: there is none).
+  struct Side {
+    const char* at;
+    int range;
+  };
+  Side ahead;                     // of the tile after the one that is loaded
+  int kbytes, steps;              // of every tile: bytes of a row that are codes or elements, and steps
+
+  // What all tiles have alike: `nk` blocks to a quad, rows of `row_bytes`.
+  __device__ __forceinline__ void shape(int nk, int row_bytes, int kbytes_, int steps_) {
+    kbytes = kbytes_;
+    steps = steps_;
+    if (!rows) {
+      stride = nk * kBlock;
+      voff = (wave >> 2) * stride + (wave & 3) * 1024 + lane * 16;
+      voff_s = wave * stride + 4096 + lane * 4;
+    } else {
+      stride = kHalf * 8 * row_bytes;
+      const int r = (wave - kHalf) * 8 + (lane >> 3);
+      voff = r * row_bytes + first;
+      voff_s = lane < kRW ? (uint32_t)(((wave - kHalf) * kRW + lane) * row_bytes) : kOob;
+    }
+  }
+  // `w`: a tile's first quad's blocks, of `nquads` there are; `x`: its first row, of `n`.
+  __device__ __forceinline__ Side side(const uint8_t* w, int nquads, const uint8_t* x, int n, int row_bytes) const {
+    if (!rows) return Side{reinterpret_cast<const char*>(w), (nquads < WP ? nquads : WP) * (int)stride};
+    return Side{reinterpret_cast<const char*>(x), n * row_bytes};
+  }
+  __device__ __forceinline__ void start(const Side& t) {
+    at = t.at;
+    at_s = at + kbytes;
+    range = t.range;
     left = kbytes;
     todo = steps;
-    if (!rows) {
-      at = reinterpret_cast<const char*>(w);
-      stride = nk * kBlock;
-      range = nquads < WP ? nquads * (int)stride : WP * (int)stride;
-      voff = (wave >> 2) * stride + (wave & 3) * 1024 + ln * 16;
-      voff_s = wave * stride + 4096 + ln * 4;
-    } else {
-      at = reinterpret_cast<const char*>(x);
-      at_s = at + kbytes;
-      stride = kHalf * 8 * row_bytes;
-      range = n * row_bytes;
-      const int r = (wave - kHalf) * 8 + (ln >> 3);
-      voff = r * row_bytes + first;
-      voff_s = ln < kRW ? (uint32_t)(((wave - kHalf) * kRW + ln) * row_bytes) : kOob;
-    }
   }
 
   // The loads of the next step.  Past the end everything is out of range, and zeros are loaded.
-  template <class F>
-  __device__ __forceinline__ void load(F more) {
-    more();
+  __device__ __forceinline__ void load() {
+    if (todo == 0 && ahead.range) start(ahead);
     const uint64_t p = reinterpret_cast<uint64_t>(at);
     const i32x4 rs{(int)p, (int)(p >> 32) & 0xFFFF, left > 0 ? range : 0, kBufferFlags};
     if (!rows) {
@@ -392,9 +403,8 @@ struct W4Pipe {
     asm volatile("" ::: "memory");
   }
 
-  template <class F>
-  __device__ __forceinline__ void begin(F more) {
-    for (int i = 0; i < (rows ? NQ : NP); ++i) load(more);
+  __device__ __forceinline__ void begin() {
+    for (int i = 0; i < (rows ? NQ : NP); ++i) load();
     wait<1, 0>(false);
   }
 
@@ -418,8 +428,8 @@ struct W4Pipe {
 
   // The next `nk` steps.  `live`: how many of the wave's rows there are; where they are not ALL, the matrix
   // instructions of the rest are left out.  `younger`: at least STORES stores went out since the last step.
-  template <bool ALL, int STORES, class F>
-  __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF], F more) {
+  template <bool ALL, int STORES>
+  __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF]) {
     if constexpr (Q8) {
       constexpr int kRing = QF >= 4 ? 4 : 2, kRead = QF > 1 ? kRing / 2 : 1;        // fragments read ahead
       i32x4 p[4], pn[4];
@@ -433,7 +443,7 @@ struct W4Pipe {
         times<QF>([&](auto q) {
           if constexpr (q == QF - kRead) {
             wait<2, STORES>(younger && i == 0);
-            load(more);
+            load();
             times<4>([&](auto f) { pn[f] = codes(np, f); });
             psn = scales(np);
           }
@@ -466,7 +476,7 @@ struct W4Pipe {
           constexpr int kn = (k + 1) % 4;
           if constexpr (k == 3) {
             wait<2, STORES>(younger && i == 0);
-            load(more);
+            load();
             read(np);
           }
           times<QF>([&](auto q) { x[(k + 1) % 2][q] = rows16(k == 3 ? nq : cq, q, kn); });
@@ -502,18 +512,19 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
   RowTiles<BQ> queue(a.plan, a.s, lane, (quads + kQuads - 1) / kQuads, a.tiles_bound);
   queue.look_up(0, true);
   Tiles pipe(smem, wave, lane);
-  auto start = [&](const typename RowTiles<BQ>::Tile& t) {
+  auto side = [&](const typename RowTiles<BQ>::Tile& t) {
     const uint8_t* W = t.w < a.s.E ? a.home + t.w * a.pitch : a.slot + (t.w - a.s.E) * a.pitch;
     if (OP == W4_FWD2) W += gate_up_bytes(a.H, a.I);
     const int q0 = t.tn * kQuads;
-    pipe.start(W + (int64_t)q0 * steps * kBlock, quads - q0, steps, a.in + t.row * a.in_row, t.rows, (int)a.in_row,
-               Q8 ? K : 2 * K, nk);
+    return pipe.side(W + (int64_t)q0 * steps * kBlock, quads - q0, a.in + t.row * a.in_row, t.rows, (int)a.in_row);
   };
   auto cur = queue.tile(0), nxt = queue.tile(1);
   if (!cur.rows) return;
-  auto more = [&] { if (pipe.todo == 0 && nxt.rows) start(nxt); };
-  start(cur);
-  pipe.begin(more);
+  pipe.shape(steps, (int)a.in_row, Q8 ? K : 2 * K, nk);
+  pipe.start(side(cur));
+  pipe.ahead = side(nxt);
+  if (!nxt.rows) pipe.ahead.range = 0;
+  pipe.begin();
   for (int round = 1;; ++round) {
     f32x4 acc[4][QF];
     clear(acc);
@@ -521,8 +532,8 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
     const int quad = t.tn * kQuads + wp;
     const int live = quad < quads ? t.rows - wq * QF * 16 : 0;
     constexpr int kStores = 4 * QF;
-    if (live >= QF * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc, more);
-    else pipe.template run<false, kStores>(nk, live, round > 1, acc, more);
+    if (live >= QF * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc);
+    else pipe.template run<false, kStores>(nk, live, round > 1, acc);
     // what the results' places are made of is worked out here, not kept during the products
     const int ln = here(lane);
     const Window out(a.out + t.row * a.out_row), gu(a.gu + (int64_t)t.row * 2 * a.I);
@@ -539,6 +550,8 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
     if (!nxt.rows) break;
     cur = nxt;
     nxt = queue.tile(round + 1);
+    pipe.ahead = side(nxt);
+    if (!nxt.rows) pipe.ahead.range = 0;
   }
   settled();                      // LDS is not given up while loads may still write to it
 #endif
