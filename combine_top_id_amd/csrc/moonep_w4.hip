@@ -430,28 +430,38 @@ struct W4Pipe {
   // instructions of the rest are left out.  `younger`: at least STORES stores went out since the last step.
   template <bool ALL, int STORES>
   __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF]) {
+    // whether the wave has rows in fragment q; without any it takes part in the loads only
+    auto there = [&](int q) { return ALL || q * 16 < live; };
     if constexpr (Q8) {
       constexpr int kRing = QF >= 4 ? 4 : 2, kRead = QF > 1 ? kRing / 2 : 1;        // fragments read ahead
       i32x4 p[4], pn[4];
-      uint32_t ps, psn = 0;
+      uint32_t ps = 0, psn = 0;
       Rows8 x[kRing];
-      times<4>([&](auto f) { p[f] = codes(cp, f); });
-      ps = scales(cp);
-      times<kRead>([&](auto q) { x[q] = rows8(cq, q); });
+      if (there(0)) {
+        times<4>([&](auto f) { p[f] = codes(cp, f); });
+        ps = scales(cp);
+      }
+      times<kRead>([&](auto q) {
+        if (there(q)) x[q] = rows8(cq, q);
+      });
       for (int i = 0; i < nk; ++i) {
         const int np = cp == (NP - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NQ - 1) * kQ ? kQ0 : cq + kQ;
         times<QF>([&](auto q) {
           if constexpr (q == QF - kRead) {
             wait<2, STORES>(younger && i == 0);
             load();
-            times<4>([&](auto f) { pn[f] = codes(np, f); });
-            psn = scales(np);
+            if (there(0)) {
+              times<4>([&](auto f) { pn[f] = codes(np, f); });
+              psn = scales(np);
+            }
           }
           // QF = 1: the one place is read anew after it has been multiplied
-          if constexpr (QF > 1) x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cq : nq, (q + kRead) % QF);
-          if (ALL || q * 16 < live)
+          if constexpr (QF > 1)
+            if (there((q + kRead) % QF)) x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cq : nq, (q + kRead) % QF);
+          if (there(q))
             times<4>([&](auto f) { multiply8<f>(acc[f][q], x[q % kRing], p[f], ps); });
-          if constexpr (QF == 1) x[0] = rows8(nq, 0);
+          if constexpr (QF == 1)
+            if (there(0)) x[0] = rows8(nq, 0);
           __builtin_amdgcn_sched_barrier(0);
         });
         times<4>([&](auto f) { p[f] = pn[f]; });
@@ -467,9 +477,17 @@ struct W4Pipe {
         times<4>([&](auto f) { p[f] = codes(at, f); });
         ps = scales(at);
       };
-      read(cp);
-      times<QF>([&](auto q) { x[0][q] = rows16(cq, q, 0); });
-      times<4>([&](auto f) { w[0][f] = __builtin_bit_cast(bf16x8, expand(p[f][0], strip_scale(ps, f))); });
+      auto widen = [&](auto k) {
+        constexpr int kk = k;
+        times<4>([&](auto f) { w[kk % 2][f] = __builtin_bit_cast(bf16x8, expand(p[f][kk], strip_scale(ps, f))); });
+      };
+      if (there(0)) {
+        read(cp);
+        widen(std::integral_constant<int, 0>{});
+      }
+      times<QF>([&](auto q) {
+        if (there(q)) x[0][q] = rows16(cq, q, 0);
+      });
       for (int i = 0; i < nk; ++i) {
         const int np = cp == (NP - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NQ - 1) * kQ ? kQ0 : cq + kQ;
         times<4>([&](auto k) {
@@ -477,16 +495,18 @@ struct W4Pipe {
           if constexpr (k == 3) {
             wait<2, STORES>(younger && i == 0);
             load();
-            read(np);
+            if (there(0)) read(np);
           }
-          times<QF>([&](auto q) { x[(k + 1) % 2][q] = rows16(k == 3 ? nq : cq, q, kn); });
           times<QF>([&](auto q) {
-            if (ALL || q * 16 < live)
+            if (there(q)) x[(k + 1) % 2][q] = rows16(k == 3 ? nq : cq, q, kn);
+          });
+          times<QF>([&](auto q) {
+            if (there(q))
               times<4>([&](auto f) {
                 acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[k % 2][q], w[k % 2][f], acc[f][q], 0, 0, 0);
               });
           });
-          times<4>([&](auto f) { w[(k + 1) % 2][f] = __builtin_bit_cast(bf16x8, expand(p[f][kn], strip_scale(ps, f))); });
+          if (there(0)) widen(std::integral_constant<int, kn>{});
           __builtin_amdgcn_sched_barrier(0);
         });
         cp = np;
