@@ -11,5 +11,5 @@ from .moonep import (moonep_query, moonep_plan, moonep_plan_noalloc, moonep_disp
                      moonep_expert_ffn_bwd_data, moonep_expert_ffn_bwd_weight, moonep_expert_tile, moonep_rmsnorm,
                      moonep_rmsnorm_q8, moonep_q8_row_bytes, moonep_q8_unpack,
                      moonep_rmsnorm_bwd, moonep_w4_slab_bytes, moonep_w4_pack, moonep_w4_unpack,
-                     moonep_expert_ffn_w4, moonep_expert_ffn_w4q8, moonep_router, moonep_router_bwd, Plan,
+                     moonep_expert_ffn_w4, moonep_expert_ffn_w4q8, moonep_expert_tile_w4, moonep_router, moonep_router_bwd, Plan,
                      Sizes, MoonepError, lib, LIB_PATH, EXPORTS)

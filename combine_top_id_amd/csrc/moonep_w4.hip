@@ -248,7 +248,7 @@ __device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t to
 }
 #pragma clang diagnostic pop
 
-// A tile of BP x BQ results by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
+// A tile of BP weight rows by BQ buffer rows, by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
 // of weights and NQ of rows.
 template <int WP_, int BQ_, int WQ_, int NP_, int NQ_>
 struct W4Geometry {
@@ -577,11 +577,15 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
 #endif
 }
 
-using W4Large = W4Geometry<4, 256, 2, 3, 3>;
-using W4Tall = W4Geometry<4, 128, 2, 3, 3>;
-using W4Medium = W4Geometry<4, 64, 1, 3, 3>;
-using W4Small = W4Geometry<4, 32, 1, 3, 3>;
-using W4Few = W4Geometry<2, 16, 1, 4, 2>;          // of 2
+// Workgroups to a CU are what LDS holds.
+template <bool Q8>
+struct W4Tiles {
+  using Large = W4Geometry<4, 256, 2, 3, 3>;                               // 8-bit rows only: 1 to a CU
+  using Tall = W4Geometry<4, 128, 2, 3, 3>;                                // 1
+  using Medium = std::conditional_t<Q8, W4Geometry<4, 64, 1, 2, 2>, W4Geometry<4, 32, 1, 2, 2>>;      // 3
+  using Small = W4Geometry<2, 64, 2, 3, 3>;                                // 8-bit rows only: 3
+  using Few = W4Geometry<2, 16, 1, 4, 2>;                                  // 4, and 3 with bf16 rows
+};
 enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_FEW };
 
 template <int OP, bool Q8, class G>
@@ -595,22 +599,77 @@ hipError_t launch_tiles(W4Args a, int per_cu, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which tile: by the mean rows of an expert.
+// Which tile.  Where the weights' stream is everything, the smallest, of which the most are on their way; then the
+// smallest that still is about one round over the CUs, as long as the few steps of a tile are no more than its start
+// and its end, which other workgroups of the CU work beside; else the large ones, which read rows and weights
+// the fewest times.  An expert's group and its replicas end inside a tile: half of one to each group.
+// Measured on MI355X, us of each launch (Few, Medium, Tall; and with 8-bit rows Few, Small, Medium, Tall, Large; mean
+// rows of an expert; R 8 for 64 experts, 4 for 16, 3 for 21):
+//   64 experts, H 7168, I 2048, gate and up    1: 121, 123, 154          141, 127, 129, 133, 174
+//                                             16: 248, 262, 282          241, 243, 262, 246, 309
+//                                             64: 559, 399, 383          436, 344, 302, 280, 364
+//                                            256: 1790, 1225, 1047      1266, 844, 668, 636, 630
+//                               down          16: 129, 122, 136          128, 134, 125, 121, 142
+//                                             64: 282, 179, 185          209, 170, 163, 135, 165
+//                                            256: 928, 587, 510          640, 418, 349, 312, 315
+//   64 experts, H 2048, I 1024, gate and up    1: 23, 31, 39              26, 23, 32, 34, 50
+//                                             32: 59, 37, 62              37, 40, 42, 48, 74
+//                                             64: 94, 60, 79              60, 46, 39, 54, 82
+//                                            256: 285, 162, 179          201, 123, 102, 118, 120
+//   16 experts, H 2048, I 1024, gate and up   32: 19, 27, 28              16, 22, 23, 22, 30
+//                                            128: 46, 34, 41              33, 23, 30, 26, 38
+//                                            256: 84, 61, 65              51, 38, 33, 44, 43
+//   21 experts, H 992, I 672,   gate and up   27: 14, 17, 19              12, 14, 16, 16, 23
+//                                            110: 27, 21, 26              16, 16, 18, 19, 28
+//   64 experts, H 2048, I 1408, gate and up  768: 1182, 733, 638;   32 of H 7168, I 2048, 1024: 2339, 1525, 1369, 1061, 982
 template <int OP, bool Q8>
 W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
-  const double mean = (double)s.A / std::min<int64_t>(s.E, s.A);
-  return mean <= 12 ? W4_FEW : mean <= 32 ? W4_SMALL : mean <= 48 ? W4_MEDIUM : mean <= 512 || !Q8 ? W4_TALL : W4_LARGE;
+  const int quads = OP == W4_FWD1 ? (I + kQuadI - 1) / kQuadI : (H + kQuadH - 1) / kQuadH;
+  const int steps = steps_of(OP == W4_FWD1 ? H : I);
+  const double groups = (double)std::min<int64_t>(s.E + s.R - 1, s.A), mean = (double)s.A / std::min<int64_t>(s.E, s.A);
+  auto tiles = [&](int bq, int wp) { return std::max(groups, (double)s.A / bq + groups / 2) * ((quads + wp - 1) / wp); };
+  const bool few_steps = steps <= 32;
+  if constexpr (Q8) {
+    if (mean <= 12 || tiles(16, 2) <= 4 * kCus) return W4_FEW;
+    if (few_steps && tiles(64, 2) <= 3 * kCus) return W4_SMALL;
+    if (few_steps && tiles(64, 4) <= 3.3 * kCus) return W4_MEDIUM;
+    return tiles(256, 4) >= 8 * kCus ? W4_LARGE : W4_TALL;
+  } else {
+    if (mean <= 20 || tiles(16, 2) <= 3 * kCus) return W4_FEW;
+    return (!few_steps && mean >= 48) || tiles(128, 4) >= 10 * kCus ? W4_TALL : W4_MEDIUM;
+  }
 }
 
 template <int OP, bool Q8>
 hipError_t launch(const W4Args& a, hipStream_t st) {
-  switch (w4_tile<OP, Q8>(a.s, a.H, a.I)) {
-    case W4_LARGE:
-      if constexpr (Q8) return launch_tiles<OP, Q8, W4Large>(a, 1, st);
-    case W4_TALL: return launch_tiles<OP, Q8, W4Tall>(a, 1, st);
-    case W4_MEDIUM: return launch_tiles<OP, Q8, W4Medium>(a, Q8 ? 2 : 1, st);
-    case W4_SMALL: return launch_tiles<OP, Q8, W4Small>(a, 2, st);
-    default: return launch_tiles<OP, Q8, W4Few>(a, Q8 ? 4 : 3, st);
+  using T = W4Tiles<Q8>;
+  const W4Tile t = w4_tile<OP, Q8>(a.s, a.H, a.I);
+  if constexpr (Q8) {
+    if (t == W4_LARGE) return launch_tiles<OP, Q8, typename T::Large>(a, 1, st);
+    if (t == W4_SMALL) return launch_tiles<OP, Q8, typename T::Small>(a, 3, st);
+  }
+  switch (t) {
+    case W4_TALL: return launch_tiles<OP, Q8, typename T::Tall>(a, 1, st);
+    case W4_MEDIUM: return launch_tiles<OP, Q8, typename T::Medium>(a, 3, st);
+    default: return launch_tiles<OP, Q8, typename T::Few>(a, Q8 ? 4 : 3, st);
+  }
+}
+
+// Weight rows of a tile, half of them gate and half up in the first product, and buffer rows.
+template <bool Q8, class G>
+void tile_size(int32_t tile[2]) {
+  tile[0] = G::BP;
+  tile[1] = G::BQ;
+}
+template <int OP, bool Q8>
+void tile_size(const moonep_sizes& s, int H, int I, int32_t tile[2]) {
+  using T = W4Tiles<Q8>;
+  switch (w4_tile<OP, Q8>(s, H, I)) {
+    case W4_LARGE: return tile_size<Q8, typename T::Large>(tile);
+    case W4_TALL: return tile_size<Q8, typename T::Tall>(tile);
+    case W4_MEDIUM: return tile_size<Q8, typename T::Medium>(tile);
+    case W4_SMALL: return tile_size<Q8, typename T::Small>(tile);
+    default: return tile_size<Q8, typename T::Few>(tile);
   }
 }
 
@@ -618,6 +677,12 @@ int check_w4(int H, int I) {
   if (H <= 0 || H % 8 != 0 || I <= 0 || I % 8 != 0) return MOONEP_EINVAL;
   if (H > MOONEP_MAX_FFN || I > MOONEP_MAX_FFN) return MOONEP_ELIMIT;
   return MOONEP_OK;
+}
+
+// Tiles are counted in 32 bits, for the smallest tile.
+int check_w4_tiles(const moonep_plan_desc* plan, int H, int I) {
+  const int64_t mt = plan->sz.A / 16 + plan->sz.E + plan->sz.P_max;
+  return mt * std::max((I + kQuadI - 1) / kQuadI, (H + kQuadH - 1) / kQuadH) > INT32_MAX ? MOONEP_ELIMIT : MOONEP_OK;
 }
 
 int check_packing(const uint16_t* w, int64_t W_el, int64_t n, int H, int I, const uint8_t* w4, int64_t pitch) {
@@ -642,9 +707,8 @@ int ffn_w4(const moonep_plan_desc* plan, const uint8_t* in, int64_t in_row, int 
   if (!in || !home || !h || !y || (plan->sz.slots > 0 && !slot)) return MOONEP_EINVAL;
   const int64_t bytes = slab_bytes(H, I), rows = plan->sz.recv_rows;
   if (pitch < bytes || pitch % 16 != 0 || (act != MOONEP_ACT_SILU && act != MOONEP_ACT_GELU)) return MOONEP_EINVAL;
-  // tiles are counted in 32 bits, for the smallest tile
-  const int64_t mt = plan->sz.A / 16 + plan->sz.E + plan->sz.P_max;
-  if (mt * std::max((I + kQuadI - 1) / kQuadI, (H + kQuadH - 1) / kQuadH) > INT32_MAX) return MOONEP_ELIMIT;
+  const int rc = check_w4_tiles(plan, H, I);
+  if (rc != MOONEP_OK) return rc;
   if (!aligned(in, 16) || !aligned(home, 16) || !aligned(slot, 16) || !aligned(gu, 16) || !aligned(h, 16) || !aligned(y, 16))
     return MOONEP_EALIGN;
   // other workgroups still read what an output that overlapped an input would change
@@ -671,6 +735,19 @@ int ffn_w4(const moonep_plan_desc* plan, const uint8_t* in, int64_t in_row, int 
 using namespace moonep;
 
 extern "C" {
+
+int moonep_expert_tile_w4(const moonep_plan_desc* plan, int H, int I, int rows_q8, int product, int32_t tile[2]) {
+  int rc = check_desc(plan);
+  if (rc == MOONEP_OK) rc = check_w4(H, I);
+  if (rc == MOONEP_OK) rc = check_w4_tiles(plan, H, I);
+  if (rc != MOONEP_OK) return rc;
+  if (!tile || (rows_q8 != 0 && rows_q8 != 1) || (product != MOONEP_PRODUCT_GATE_UP && product != MOONEP_PRODUCT_DOWN) ||
+      (rows_q8 && (H % 32 != 0 || I % 32 != 0)))
+    return MOONEP_EINVAL;
+  if (rows_q8) product == MOONEP_PRODUCT_DOWN ? tile_size<W4_FWD2, true>(plan->sz, H, I, tile) : tile_size<W4_FWD1, true>(plan->sz, H, I, tile);
+  else product == MOONEP_PRODUCT_DOWN ? tile_size<W4_FWD2, false>(plan->sz, H, I, tile) : tile_size<W4_FWD1, false>(plan->sz, H, I, tile);
+  return MOONEP_OK;
+}
 
 int64_t moonep_w4_slab_bytes(int H, int I) {
   const int rc = check_w4(H, I);

@@ -84,6 +84,7 @@ def lib():
     L.moonep_w4_slab_bytes.argtypes = [i32, i32]
     L.moonep_w4_pack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
     L.moonep_w4_unpack.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp]
+    L.moonep_expert_tile_w4.argtypes = [PD, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_int32)]
     L.moonep_expert_ffn_w4.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp, vp]
     L.moonep_expert_ffn_w4q8.argtypes = [PD, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp]
     L.moonep_rmsnorm_bwd_workspace.argtypes = [i64, i32]
@@ -100,7 +101,7 @@ def lib():
               "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight", "moonep_expert_tile",
               "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_unpack", "moonep_rmsnorm_bwd",
               "moonep_w4_pack", "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8",
-              "moonep_router", "moonep_router_bwd"):
+              "moonep_expert_tile_w4", "moonep_router", "moonep_router_bwd"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -114,7 +115,8 @@ EXPORTS = ("moonep_query", "moonep_plan", "moonep_plan_noalloc", "moonep_dispatc
            "moonep_expert_ffn", "moonep_expert_ffn_bwd_data", "moonep_expert_ffn_bwd_weight",
            "moonep_expert_tile", "moonep_rmsnorm", "moonep_rmsnorm_q8", "moonep_q8_row_bytes", "moonep_q8_unpack",
            "moonep_rmsnorm_bwd_workspace", "moonep_rmsnorm_bwd", "moonep_w4_slab_bytes", "moonep_w4_pack",
-           "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8", "moonep_router", "moonep_router_bwd")
+           "moonep_w4_unpack", "moonep_expert_ffn_w4", "moonep_expert_ffn_w4q8", "moonep_expert_tile_w4",
+           "moonep_router", "moonep_router_bwd")
 
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -719,6 +721,16 @@ def moonep_expert_ffn_w4q8(plan: Plan, rows, home_w4, slot_w4, H, I, act="silu",
     _run(lib().moonep_expert_ffn_w4q8, D, ctypes.byref(plan.desc), rp, H, I, _act(act), wp, sp, pitch, hp, yp,
          _stream(stream, D))
     return y, h
+
+
+def moonep_expert_tile_w4(plan: Plan, H, I, rows_q8, product):
+    """The tile that a product ("gate_up" or "down") of moonep_expert_ffn_w4, or with `rows_q8` of moonep_expert_ffn_w4q8, is
+    computed in: weight rows and buffer rows."""
+    if product not in PRODUCTS[:2]:
+        raise MoonepError(f"product must be one of {PRODUCTS[:2]}, got {product!r}")
+    tile = (ctypes.c_int32 * 2)()
+    _check(lib().moonep_expert_tile_w4(ctypes.byref(plan.desc), H, I, int(bool(rows_q8)), PRODUCTS.index(product), tile))
+    return tile[0], tile[1]
 
 
 def _logits(logits, score):

@@ -446,6 +446,14 @@ int moonep_expert_ffn_w4q8(const moonep_plan_desc* plan, const uint8_t* rows, in
                            const uint8_t* home_w4, const uint8_t* slot_w4, int64_t W_bytes, uint8_t* h,
                            uint16_t* y, hipStream_t stream);
 
+/* The tile that a product of these two calls is computed in for these sizes, for profiles and for tests that mean a
+ * certain one.  Host only.
+ *   rows_q8  0: moonep_expert_ffn_w4; 1: moonep_expert_ffn_w4q8
+ *   product  MOONEP_PRODUCT_GATE_UP or MOONEP_PRODUCT_DOWN (EINVAL for others)
+ *   tile     host int32 [2]: weight rows (of gate and up, half of them each), buffer rows
+ * Errors of plan, H and I as in the calls. */
+int moonep_expert_tile_w4(const moonep_plan_desc* plan, int H, int I, int rows_q8, int product, int32_t tile[2]);
+
 /* The router in front of the plan, over T tokens (any T, also 0, when nothing is written): what it
  * writes is what moonep_plan takes.
  *   s = softmax(l) or sigmoid(l) of a token's E logits;  key = s + bias

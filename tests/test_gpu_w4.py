@@ -12,6 +12,7 @@ from tests import expert_ref as X
 from tests import w4_ref as W
 from tests.gpu_util import say
 from tests.test_gpu_expert_ffn import Case, bf16
+from tests.w4_tiles import TILES
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -170,6 +171,15 @@ def test_rows_in_8_bits(R, E, K, S, slots, H, I, mv, act):
     H, I = up32(H), up32(I)
     say(f"w4q8 R={R} E={E} K={K} S={S} slots={slots} H={H} I={I} maxvio={mv} {act}")
     Case4(R, E, K, S, slots, H, I, mv, 240 + R + E + S, more=32 * (R % 2)).check8(act)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("sizes,q8,product,tile", TILES)
+def test_every_tile(sizes, q8, product, tile):
+    say(f"tile {tile} of {product}, rows in {8 if q8 else 16} bits: {sizes}")
+    c = Case4(*sizes, 340 + sizes[3])
+    assert M.moonep_expert_tile_w4(c.plan, c.H, c.I, q8, product) == tile
+    (c.check8 if q8 else c.check16)("silu")
     torch.cuda.synchronize()
 
 
