@@ -250,9 +250,10 @@ __device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t to
 
 // A tile of BP weight rows by BQ buffer rows, by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
 // of weights and NQ of rows.
-template <int WP_, int BQ_, int WQ_, int NP_, int NQ_>
+template <int WP_, int BQ_, int WQ_, int NP_, int NQ_, int PER_CU_>
 struct W4Geometry {
   static constexpr int WP = WP_, WQ = WQ_, NW = WP * WQ, BP = 64 * WP, BQ = BQ_, QF = BQ / WQ / 16, NP = NP_, NQ = NQ_;
+  static constexpr int PER_CU = PER_CU_;         // workgroups, in LDS and in registers
 };
 
 // The products of one tile after another, without a break between them.  LDS holds NP steps of 128 k of weights, the
@@ -273,19 +274,22 @@ struct W4Pipe {
   static constexpr int QF = G::QF, NW = G::NW, BQ = G::BQ, WP = G::WP, NP = G::NP, NQ = G::NQ;
   static constexpr int kLines = Q8 ? 1 : 2;                          // of 128 bytes of a row
   static constexpr int kHalf = NW / 2;                               // waves that load one side
-  static constexpr int kRW = BQ / kHalf;                             // rows whose scales a wave loads
-  static constexpr int kP = WP * kBlock, kQB = kLines * BQ * 128, kQ = kQB + (Q8 ? kHalf * 256 : 0);
-  static constexpr int kQ0 = NP * kP, kLds = NP * kP + NQ * kQ;
+  static constexpr int kP = WP * kBlock, kQ = kLines * BQ * 128, kQ0 = NP * kP;
+  // the scales of rows in 8 bits: 16 bytes of each for four steps, NQ times four steps of a tile, or what there is
+  static constexpr int kSW = Q8 ? (BQ + 63) / 64 : 0, kS = kSW * 1024, kS0 = kQ0 + NQ * kQ, kLds = kS0 + NQ * kS;
   static constexpr int kCP = WP * 4 / kHalf, kSP = WP / kHalf, kLP = kCP + kSP;      // a wave's loads of a step
-  static constexpr int kCQ = kQB / 1024 / kHalf, kLQ = kCQ + (Q8 ? 1 : 0);
-  static_assert(kHalf >= 1 && kCP * kHalf == WP * 4 && kSP * kHalf == WP && kCQ * kHalf * 1024 == kQB && kRW <= 64 &&
-                kLds <= 160 * 1024 && NP >= 2 && NQ >= 2 && (NP - 1) * kLP < 48 && (NQ - 1) * kLQ < 48);
+  // not counting the scales of rows: these are started before the others of a step, and so are waited for too early, if
+  // at all
+  static constexpr int kCQ = kQ / 1024 / kHalf, kLQ = kCQ;
+  static_assert(kHalf >= 1 && kCP * kHalf == WP * 4 && kSP * kHalf == WP && kCQ * kHalf * 1024 == kQ && kSW <= kHalf &&
+                NP >= 2 && NQ >= 2 && G::PER_CU * kLds <= 160 * 1024 && (NP - 1) * kLP < 48 && (NQ - 1) * kLQ < 48);
   static constexpr int kSteps = NP > NQ ? NP : NQ;                   // loads are that far ahead
   uint32_t lds;                   // LDS
   int wave, lane;
   bool rows;                      // this wave loads rows (uniform)
   int lane_p, lane_q, lane_s;     // this lane's first LDS byte of a fragment of weights, of rows, of a row's scale
-  int cp, cq;                     // the current step's places in LDS
+  int cp, cq, cs;                 // the current step's places in LDS
+  int scaling;                    // where the next four steps' scales are loaded to
   uint32_t voff, voff_s;          // this lane's first load and its scale's
   uint32_t stride;                // bytes from a quad to the next, or of kHalf * 8 rows (uniform)
   const char *at, *at_s;          // the next step to load
@@ -303,9 +307,9 @@ struct W4Pipe {
     lane_p = base + wave % WP * kBlock + lane * 16;
     const int row = wave / WP * QF * 16 + c;
     lane_q = base + row * 128 + ((g ^ (row & 7)) << 4);
-    lane_s = base + kQB + scale_at(row) + g;
+    lane_s = base + row * 16 + g;
+    cs = scaling = kS0;
   }
-  static __device__ __forceinline__ int scale_at(int row) { return row / kRW * 256 + row % kRW * 4; }
 
   // One side of a tile: where it begins, and its bytes (0: there is none).
   struct Side {
@@ -327,7 +331,7 @@ struct W4Pipe {
       stride = kHalf * 8 * row_bytes;
       const int r = (wave - kHalf) * 8 + (lane >> 3);
       voff = r * row_bytes + first;
-      voff_s = lane < kRW ? (uint32_t)(((wave - kHalf) * kRW + lane) * row_bytes) : kOob;
+      voff_s = (uint32_t)(((wave - kHalf) * 64 + lane) * row_bytes);
     }
   }
   // `w`: a tile's first quad's blocks, of `nquads` there are; `x`: its first row, of `n`.
@@ -361,6 +365,19 @@ struct W4Pipe {
       range -= kBlock;
       loading = loading == (NP - 1) * kP ? 0 : loading + kP;
     } else {
+      if constexpr (Q8) {
+        const int step = steps - todo;
+        if (step % 4 == 0) {
+          if (wave - kHalf < kSW) {
+            const uint64_t s = reinterpret_cast<uint64_t>(at_s);
+            // to the end of the tile's last row
+            const i32x4 r{(int)s, (int)(s >> 32) & 0xFFFF, left > 0 ? range - (int)(at_s - at) : 0, kBufferFlags};
+            load_lds<0>(r, voff_s, uni(lds + scaling + (wave - kHalf) * 1024));
+          }
+          at_s += 16;
+          scaling = scaling == kS0 + (NQ - 1) * kS ? kS0 : scaling + kS;
+        }
+      }
       const uint32_t to = uni(lds + loading + (wave - kHalf) * 1024);
       times<kCQ>([&](auto i) {                // eight rows of a line of 128 bytes
         constexpr int kLine = i * kHalf / (BQ / 8), kRow = i * kHalf % (BQ / 8) / kHalf;
@@ -369,12 +386,6 @@ struct W4Pipe {
         const uint32_t v = voff + kRow * stride + kSkip;
         load_lds<i * kHalf * 1024>(rs, first + kSkip < left ? v : kOob, to);
       });
-      if constexpr (Q8) {
-        const uint64_t s = reinterpret_cast<uint64_t>(at_s);
-        const i32x4 r{(int)s, (int)(s >> 32) & 0xFFFF, left > 0 ? scale_range() : 0, kBufferFlags};
-        load_lds4(r, voff_s, uni(lds + loading + kQB + (wave - kHalf) * 256));
-        at_s += 4;
-      }
       at += kLines * 128;
       range -= kLines * 128;
       loading = loading == kQ0 + (NQ - 1) * kQ ? kQ0 : loading + kQ;
@@ -382,10 +393,6 @@ struct W4Pipe {
     left -= kLines * 128;
     --todo;
   }
-  // From a row's scales of the next step to the tile's end, which is that of its last row: left bytes of codes, and
-  // the scales that have been loaded.
-  __device__ __forceinline__ int scale_range() const { return range - (int)(at_s - at); }
-
   // Waits until at most `steps` steps of this wave's loads are on their way, and, where `younger` is set, the STORES
   // stores that went out after them.
   template <int LESS, int STORES>
@@ -409,9 +416,9 @@ struct W4Pipe {
   }
 
   struct Rows8 { i32x4 lo, hi; int scale; };
-  __device__ __forceinline__ Rows8 rows8(int at, int q) const {
+  __device__ __forceinline__ Rows8 rows8(int at, int scale, int q) const {
     const int x = lane_q + at, y = x ^ 64;
-    return Rows8{*(const LDS i32x4*)(x + q * 2048), *(const LDS i32x4*)(y + q * 2048), *(const LDS uint8_t*)(lane_s + at + (scale_at(q * 16) - scale_at(0)))};
+    return Rows8{*(const LDS i32x4*)(x + q * 2048), *(const LDS i32x4*)(y + q * 2048), *(const LDS uint8_t*)(lane_s + scale + q * 256)};
   }
   __device__ __forceinline__ bf16x8 rows16(int at, int q, int i) const {
     return *(const LDS bf16x8*)(((lane_q + at) ^ (i & 1) << 6) + (i >> 1) * BQ * 128 + q * 2048);
@@ -442,10 +449,12 @@ struct W4Pipe {
         ps = scales(cp);
       }
       times<kRead>([&](auto q) {
-        if (there(q)) x[q] = rows8(cq, q);
+        if (there(q)) x[q] = rows8(cq, cs, q);
       });
       for (int i = 0; i < nk; ++i) {
         const int np = cp == (NP - 1) * kP ? 0 : cp + kP, nq = cq == kQ0 + (NQ - 1) * kQ ? kQ0 : cq + kQ;
+        const int four = cs - i % 4 * 4;         // these four steps' scales, then this tile's next, or another's first
+        const int ns = i % 4 < 3 && i + 1 < nk ? cs + 4 : four == kS0 + (NQ - 1) * kS ? kS0 : four + kS;
         times<QF>([&](auto q) {
           if constexpr (q == QF - kRead) {
             wait<2, STORES>(younger && i == 0);
@@ -457,17 +466,18 @@ struct W4Pipe {
           }
           // QF = 1: the one place is read anew after it has been multiplied
           if constexpr (QF > 1)
-            if (there((q + kRead) % QF)) x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cq : nq, (q + kRead) % QF);
+            if (there((q + kRead) % QF)) x[(q + kRead) % kRing] = rows8(q + kRead < QF ? cq : nq, q + kRead < QF ? cs : ns, (q + kRead) % QF);
           if (there(q))
             times<4>([&](auto f) { multiply8<f>(acc[f][q], x[q % kRing], p[f], ps); });
           if constexpr (QF == 1)
-            if (there(0)) x[0] = rows8(nq, 0);
+            if (there(0)) x[0] = rows8(nq, ns, 0);
           __builtin_amdgcn_sched_barrier(0);
         });
         times<4>([&](auto f) { p[f] = pn[f]; });
         ps = psn;
         cp = np;
         cq = nq;
+        cs = ns;
       }
     } else {
       i32x4 p[4];
@@ -517,7 +527,7 @@ struct W4Pipe {
 };
 
 template <int OP, bool Q8, class G>
-__global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
+__global__ __launch_bounds__(64 * G::NW, G::PER_CU * G::NW / 4 > 2 ? G::PER_CU * G::NW / 4 : 2) void tile_kernel(const W4Args a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int BQ = G::BQ, WP = G::WP, QF = G::QF;
   constexpr int kQuads = G::BP / 64;
@@ -577,24 +587,23 @@ __global__ __launch_bounds__(64 * G::NW, 2) void tile_kernel(const W4Args a) {
 #endif
 }
 
-// Workgroups to a CU are what LDS holds.
 template <bool Q8>
 struct W4Tiles {
-  using Large = W4Geometry<4, 256, 2, 3, 3>;                               // 8-bit rows only: 1 to a CU
-  using Tall = W4Geometry<4, 128, 2, 3, 3>;                                // 1
-  using Medium = std::conditional_t<Q8, W4Geometry<4, 64, 1, 2, 2>, W4Geometry<4, 32, 1, 2, 2>>;      // 3
-  using Small = W4Geometry<2, 64, 2, 3, 3>;                                // 8-bit rows only: 3
-  using Few = W4Geometry<2, 16, 1, 4, 2>;                                  // 4, and 3 with bf16 rows
+  using Large = W4Geometry<4, 256, 2, 3, 3, 1>;                            // 8-bit rows only
+  using Tall = W4Geometry<4, 128, 2, 3, 3, 1>;
+  using Medium = std::conditional_t<Q8, W4Geometry<4, 64, 1, 2, 2, 3>, W4Geometry<4, 32, 1, 2, 2, 3>>;
+  using Small = W4Geometry<2, 64, 2, 3, 3, 3>;                             // 8-bit rows only
+  using Few = W4Geometry<2, 16, 1, 4, 2, Q8 ? 4 : 3>;
 };
 enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_FEW };
 
 template <int OP, bool Q8, class G>
-hipError_t launch_tiles(W4Args a, int per_cu, hipStream_t st) {
+hipError_t launch_tiles(W4Args a, hipStream_t st) {
   constexpr int kQuads = G::BP / 64;
   const int64_t mt = a.s.A / G::BQ + std::min<int64_t>(a.s.E + a.s.P_max, a.s.A);
   const int quads = OP == W4_FWD1 ? (a.I + kQuadI - 1) / kQuadI : (a.H + kQuadH - 1) / kQuadH;
   a.tiles_bound = (int)mt;
-  const int grid = (int)std::min<int64_t>((mt * ((quads + kQuads - 1) / kQuads) + 7) / 8 * 8, per_cu * kCus);
+  const int grid = (int)std::min<int64_t>((mt * ((quads + kQuads - 1) / kQuads) + 7) / 8 * 8, G::PER_CU * kCus);
   hipLaunchKernelGGL((tile_kernel<OP, Q8, G>), dim3(grid), dim3(64 * G::NW), 0, st, a);
   return hipGetLastError();
 }
@@ -645,13 +654,13 @@ hipError_t launch(const W4Args& a, hipStream_t st) {
   using T = W4Tiles<Q8>;
   const W4Tile t = w4_tile<OP, Q8>(a.s, a.H, a.I);
   if constexpr (Q8) {
-    if (t == W4_LARGE) return launch_tiles<OP, Q8, typename T::Large>(a, 1, st);
-    if (t == W4_SMALL) return launch_tiles<OP, Q8, typename T::Small>(a, 3, st);
+    if (t == W4_LARGE) return launch_tiles<OP, Q8, typename T::Large>(a, st);
+    if (t == W4_SMALL) return launch_tiles<OP, Q8, typename T::Small>(a, st);
   }
   switch (t) {
-    case W4_TALL: return launch_tiles<OP, Q8, typename T::Tall>(a, 1, st);
-    case W4_MEDIUM: return launch_tiles<OP, Q8, typename T::Medium>(a, 3, st);
-    default: return launch_tiles<OP, Q8, typename T::Few>(a, Q8 ? 4 : 3, st);
+    case W4_TALL: return launch_tiles<OP, Q8, typename T::Tall>(a, st);
+    case W4_MEDIUM: return launch_tiles<OP, Q8, typename T::Medium>(a, st);
+    default: return launch_tiles<OP, Q8, typename T::Few>(a, st);
   }
 }
 
