@@ -271,7 +271,7 @@ struct W4Geometry {
 // starts the loads of the step NP (or NQ) further on over it.  One barrier a step.
 template <bool Q8, class G>
 struct W4Pipe {
-  static constexpr int QF = G::QF, NW = G::NW, BQ = G::BQ, WP = G::WP, NP = G::NP, NQ = G::NQ;
+  static constexpr int QF = G::QF, NW = G::NW, BQ = G::BQ, WP = G::WP, WQ = G::WQ, NP = G::NP, NQ = G::NQ;
   static constexpr int kLines = Q8 ? 1 : 2;                          // of 128 bytes of a row
   static constexpr int kHalf = NW / 2;                               // waves that load one side
   static constexpr int kP = WP * kBlock, kQ = kLines * BQ * 128, kQ0 = NP * kP;
@@ -305,7 +305,7 @@ struct W4Pipe {
     const int chunk = (lane & 7) ^ (lane >> 3);
     first = Q8 ? chunk * 16 : (chunk & 3) * 64 + (chunk >> 2) * 16;
     lane_p = base + wave % WP * kBlock + lane * 16;
-    const int row = wave / WP * QF * 16 + c;
+    const int row = wave / WP * 16 + c;
     lane_q = base + row * 128 + ((g ^ (row & 7)) << 4);
     lane_s = base + row * 16 + g;
     cs = scaling = kS0;
@@ -418,10 +418,11 @@ struct W4Pipe {
   struct Rows8 { i32x4 lo, hi; int scale; };
   __device__ __forceinline__ Rows8 rows8(int at, int scale, int q) const {
     const int x = lane_q + at, y = x ^ 64;
-    return Rows8{*(const LDS i32x4*)(x + q * 2048), *(const LDS i32x4*)(y + q * 2048), *(const LDS uint8_t*)(lane_s + scale + q * 256)};
+    return Rows8{*(const LDS i32x4*)(x + q * WQ * 2048), *(const LDS i32x4*)(y + q * WQ * 2048),
+                 *(const LDS uint8_t*)(lane_s + scale + q * WQ * 256)};
   }
   __device__ __forceinline__ bf16x8 rows16(int at, int q, int i) const {
-    return *(const LDS bf16x8*)(((lane_q + at) ^ (i & 1) << 6) + (i >> 1) * BQ * 128 + q * 2048);
+    return *(const LDS bf16x8*)(((lane_q + at) ^ (i & 1) << 6) + (i >> 1) * BQ * 128 + q * WQ * 2048);
   }
   __device__ __forceinline__ i32x4 codes(int at, int f) const { return *(const LDS i32x4*)(lane_p + at + f * 1024); }
   __device__ __forceinline__ uint32_t scales(int at) const { return *(const LDS uint32_t*)((lane_p - lane * 12) + at + 4096); }
@@ -433,12 +434,12 @@ struct W4Pipe {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xw, pw, acc, 0, 4, 0, x.scale, F, (int)scales);
   }
 
-  // The next `nk` steps.  `live`: how many of the wave's rows there are; where they are not ALL, the matrix
-  // instructions of the rest are left out.  `younger`: at least STORES stores went out since the last step.
+  // The next `nk` steps.  `live`: how many of the tile's rows there are from the wave's first on; where it has not ALL of its
+  // fragments, the matrix instructions of the rest are left out.  `younger`: at least STORES stores went out since the last step.
   template <bool ALL, int STORES>
   __device__ __forceinline__ void run(int nk, int live, bool younger, f32x4 (&acc)[4][QF]) {
     // whether the wave has rows in fragment q; without any it takes part in the loads only
-    auto there = [&](int q) { return ALL || q * 16 < live; };
+    auto there = [&](int q) { return ALL || q * WQ * 16 < live; };
     if constexpr (Q8) {
       constexpr int kRing = QF >= 4 ? 4 : 2, kRead = QF > 1 ? kRing / 2 : 1;        // fragments read ahead
       i32x4 p[4], pn[4];
@@ -560,9 +561,9 @@ __global__ __launch_bounds__(64 * G::NW, G::PER_CU * G::NW / 4 > 2 ? G::PER_CU *
     clear(acc);
     const auto t = cur;
     const int quad = t.tn * kQuads + wp;
-    const int live = quad < quads ? t.rows - wq * QF * 16 : 0;
+    const int live = quad < quads ? t.rows - wq * 16 : 0;
     constexpr int kStores = 4 * QF;
-    if (live >= QF * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc);
+    if (live > (QF - 1) * G::WQ * 16) pipe.template run<true, kStores>(nk, live, round > 1, acc);
     else pipe.template run<false, kStores>(nk, live, round > 1, acc);
     // what the results' places are made of is worked out here, not kept during the products
     const int ln = here(lane);
@@ -571,7 +572,7 @@ __global__ __launch_bounds__(64 * G::NW, G::PER_CU * G::NW / 4 > 2 ? G::PER_CU *
     for (int q = 0; q < QF; ++q) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = (wq * QF + q) * 16 + (ln >> 4) * 4 + i;
+        const int r = (q * G::WQ + wq) * 16 + (ln >> 4) * 4 + i;
         put<OP, Q8>(a, out, gu, f32x4{acc[0][q][i], acc[1][q][i], acc[2][q][i], acc[3][q][i]}, r,
                     r < t.rows && quad < quads, quad, ln & 15);
       }
