@@ -239,15 +239,6 @@ __device__ __forceinline__ void put(const W4Args& a, const Window& out, const Wi
 #endif
 }
 
-// 4 bytes a lane from the buffer straight into LDS, to `to` + lane * 4 (see load_lds).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void load_lds4(i32x4 rsrc, uint32_t voff, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(to), "v"(voff), "s"(rsrc) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
 // A tile of BP weight rows by BQ buffer rows, by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
 // of weights and NQ of rows.
 template <int WP_, int BQ_, int WQ_, int NP_, int NQ_, int PER_CU_>
@@ -277,17 +268,18 @@ struct W4Pipe {
   static constexpr int kP = WP * kBlock, kQ = kLines * BQ * 128, kQ0 = NP * kP;
   // the scales of rows in 8 bits: 16 bytes of each for four steps, NQ times four steps of a tile, or what there is
   static constexpr int kSW = Q8 ? (BQ + 63) / 64 : 0, kS = kSW * 1024, kS0 = kQ0 + NQ * kQ, kLds = kS0 + NQ * kS;
-  static constexpr int kCP = WP * 4 / kHalf, kSP = WP / kHalf, kLP = kCP + kSP;      // a wave's loads of a step
+  static constexpr int kCP = WP * 4 / kHalf, kLP = kCP + 1;          // loads of a step: codes, and the first wave's scales
   // not counting the scales of rows: these are started before the others of a step, and so are waited for too early, if
   // at all
   static constexpr int kCQ = kQ / 1024 / kHalf, kLQ = kCQ;
-  static_assert(kHalf >= 1 && kCP * kHalf == WP * 4 && kSP * kHalf == WP && kCQ * kHalf * 1024 == kQ && kSW <= kHalf &&
+  static_assert(kHalf >= 1 && kCP * kHalf == WP * 4 && WP <= 4 && kCQ * kHalf * 1024 == kQ && kSW <= kHalf &&
                 NP >= 2 && NQ >= 2 && G::PER_CU * kLds <= 160 * 1024 && (NP - 1) * kLP < 48 && (NQ - 1) * kLQ < 48);
   static constexpr int kSteps = NP > NQ ? NP : NQ;                   // loads are that far ahead
   uint32_t lds;                   // LDS
   int wave, lane;
   bool rows;                      // this wave loads rows (uniform)
-  int lane_p, lane_q, lane_s;     // this lane's first LDS byte of a fragment of weights, of rows, of a row's scale
+  int lane_p, lane_ps;            // this lane's first LDS byte of a fragment of weights, of their scales,
+  int lane_q, lane_s;             // of a fragment of rows, of a row's scale
   int cp, cq, cs;                 // the current step's places in LDS
   int scaling;                    // where the next four steps' scales are loaded to
   uint32_t voff, voff_s;          // this lane's first load and its scale's
@@ -304,7 +296,8 @@ struct W4Pipe {
     loading = rows ? kQ0 : 0;
     const int chunk = (lane & 7) ^ (lane >> 3);
     first = Q8 ? chunk * 16 : (chunk & 3) * 64 + (chunk >> 2) * 16;
-    lane_p = base + wave % WP * kBlock + lane * 16;
+    lane_p = base + wave % WP * 4096 + lane * 16;
+    lane_ps = base + WP * 4096 + wave % WP * 256 + lane * 4;
     const int row = wave / WP * 16 + c;
     lane_q = base + row * 128 + ((g ^ (row & 7)) << 4);
     lane_s = base + row * 16 + g;
@@ -326,7 +319,7 @@ struct W4Pipe {
     if (!rows) {
       stride = nk * kBlock;
       voff = (wave >> 2) * stride + (wave & 3) * 1024 + lane * 16;
-      voff_s = wave * stride + 4096 + lane * 4;
+      voff_s = (lane >> 4) * stride + 4096 + (lane & 15) * 16;
     } else {
       stride = kHalf * 8 * row_bytes;
       const int r = (wave - kHalf) * 8 + (lane >> 3);
@@ -353,14 +346,12 @@ struct W4Pipe {
     const uint64_t p = reinterpret_cast<uint64_t>(at);
     const i32x4 rs{(int)p, (int)(p >> 32) & 0xFFFF, left > 0 ? range : 0, kBufferFlags};
     if (!rows) {
-      // chunk i * kHalf + wave of the step's, strip by strip
-      const uint32_t to = uni(lds + loading + (wave >> 2) * kBlock + (wave & 3) * 1024);
+      // chunk i * kHalf + wave of the step's, strip by strip; 16 lanes a quad's scales
+      const uint32_t to = uni(lds + loading + wave * 1024);
       times<kCP>([&](auto i) {
-        load_lds<(i * kHalf >> 2) * kBlock + (i * kHalf & 3) * 1024>(rs, voff + (i * kHalf >> 2) * stride + (i * kHalf & 3) * 1024, to);
+        load_lds<i * kHalf * 1024>(rs, voff + (i * kHalf >> 2) * stride + (i * kHalf & 3) * 1024, to);
       });
-      times<kSP>([&](auto i) {
-        load_lds4(rs, voff_s + i * kHalf * stride, uni(lds + loading + (i * kHalf + wave) * kBlock + 4096));
-      });
+      if (wave == 0 && (WP == 4 || lane < WP * 16)) load_lds<WP * 4096>(rs, voff_s, to);
       at += kBlock;
       range -= kBlock;
       loading = loading == (NP - 1) * kP ? 0 : loading + kP;
@@ -393,19 +384,19 @@ struct W4Pipe {
     left -= kLines * 128;
     --todo;
   }
-  // Waits until at most `steps` steps of this wave's loads are on their way, and, where `younger` is set, the STORES
+  // Waits until at most N - LESS steps of this wave's loads are on their way, and, where `younger` is set, the STORES
   // stores that went out after them.
   template <int LESS, int STORES>
   __device__ __forceinline__ void wait(bool younger) {
-    constexpr int kMoreP = (NP - LESS) * kLP + STORES, kMoreQ = (NQ - LESS) * kLQ + STORES;
     asm volatile("" ::: "memory");
-    if (younger) {
-      if (!rows) __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMoreP < 63 ? kMoreP : 63));
-      else __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMoreQ < 63 ? kMoreQ : 63));
-    } else {
-      if (!rows) __builtin_amdgcn_s_waitcnt(wait_vm_lds((NP - LESS) * kLP));
-      else __builtin_amdgcn_s_waitcnt(wait_vm_lds((NQ - LESS) * kLQ));
-    }
+    auto until = [&](auto loads) {
+      constexpr int kMore = loads + STORES;
+      if (younger) __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMore < 63 ? kMore : 63));
+      else __builtin_amdgcn_s_waitcnt(wait_vm_lds(loads));
+    };
+    if (rows) until(std::integral_constant<int, (NQ - LESS) * kLQ>{});
+    else if (wave == 0) until(std::integral_constant<int, (NP - LESS) * kLP>{});
+    else until(std::integral_constant<int, (NP - LESS) * kCP>{});
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
@@ -425,7 +416,7 @@ struct W4Pipe {
     return *(const LDS bf16x8*)(((lane_q + at) ^ (i & 1) << 6) + (i >> 1) * BQ * 128 + q * WQ * 2048);
   }
   __device__ __forceinline__ i32x4 codes(int at, int f) const { return *(const LDS i32x4*)(lane_p + at + f * 1024); }
-  __device__ __forceinline__ uint32_t scales(int at) const { return *(const LDS uint32_t*)((lane_p - lane * 12) + at + 4096); }
+  __device__ __forceinline__ uint32_t scales(int at) const { return *(const LDS uint32_t*)(lane_ps + at); }
 
   template <int F>
   static __device__ __forceinline__ void multiply8(f32x4& acc, const Rows8& x, const i32x4& p, uint32_t scales) {
