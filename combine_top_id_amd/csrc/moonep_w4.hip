@@ -210,6 +210,7 @@ __device__ __forceinline__ void put(const W4Args& a, const Window& out, const Wi
     const int col = quad * kQuadH + 4 * c;
     out.store(u32x2{bf2(d[0], d[1]), bf2(d[2], d[3])}, in && col < a.H ? at + col * 2 : kOob);
   } else {
+    // h in bf16 is rounded once, to 2^-8 of it: the second product's instructions take bf16
     const int col = quad * kQuadI + 2 * c;
     float slope;
     const float h0 = act_of(d[0], a.act, &slope) * d[2], h1 = act_of(d[1], a.act, &slope) * d[3];
@@ -223,7 +224,8 @@ __device__ __forceinline__ void put(const W4Args& a, const Window& out, const Wi
       }
     } else {
       // the rule of the 8-bit norm: the smallest power of two that brings the largest of the 32 to 448 =
-      // 1.75 * 2^8 or less
+      // 1.75 * 2^8 or less.  h is rounded here once, to half a step of 2^-4 of it: half the bytes of bf16, and the second
+      // product's instructions take no wider rows
       const uint32_t b = __float_as_uint(row_max(fmaxf(fabsf(h0), fabsf(h1))));
       const int ex = max((int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u), 0);
       const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
@@ -239,8 +241,8 @@ __device__ __forceinline__ void put(const W4Args& a, const Window& out, const Wi
 #endif
 }
 
-// A tile of BP weight rows by BQ buffer rows, by WP x WQ waves, each a quad of weights by QF fragments of 16 rows; LDS holds NP steps
-// of weights and NQ of rows.
+// A tile of BP weight rows by BQ buffer rows, by WP x WQ waves: wave (p, q) has quad p of the weights and every WQ-th fragment
+// of 16 rows from q on, so that a tile with few rows leaves work to all.  LDS holds NP steps of weights and NQ of rows.
 template <int WP_, int BQ_, int WQ_, int NP_, int NQ_, int PER_CU_>
 struct W4Geometry {
   static constexpr int WP = WP_, WQ = WQ_, NW = WP * WQ, BP = 64 * WP, BQ = BQ_, QF = BQ / WQ / 16, NP = NP_, NQ = NQ_;
@@ -260,6 +262,15 @@ struct W4Geometry {
 // A step is cut into parts; in each, the operands of a later part are read from LDS into registers among its matrix
 // instructions.  When all of a step has been read, every wave waits for the next step's loads and for the others, and
 // starts the loads of the step NP (or NQ) further on over it.  One barrier a step.
+//
+// What bounds it, measured on MI355X (us of a gate and up launch with loads or matrix instructions left out, sums wrong):
+//   32 experts of H 7168, I 2048, 1024 8-bit rows each, 256 x 256 tiles: 1023 (1.9 PFLOP/s, of 2.7 that a large 8-bit library
+//     product reaches); 767 without matrix instructions, 790 without loads, 800 without those of rows, 931 without those of
+//     weights: both sides take three quarters of the time and hide behind each other for half of it
+//   64 experts, 64 rows each, both launches 389: 353 without loads of rows, 302 without those of weights, and no less
+//     without matrix instructions: a step's latencies, which two waves a SIMD do not hide
+//   64 experts, a row to most of them, both launches 190: the weights' stream, 0.98 GB at 5.2 TB/s; 182 without scales, which
+//     are 6% of its bytes
 template <bool Q8, class G>
 struct W4Pipe {
   static constexpr int QF = G::QF, NW = G::NW, BQ = G::BQ, WP = G::WP, WQ = G::WQ, NP = G::NP, NQ = G::NQ;

@@ -181,6 +181,21 @@ def test_many_tokens():
         assert torch.equal(M.moonep_router_bwd(l[at:at + 10].clone(), ids[at:at + 10].clone(), w[at:at + 10].clone()), g[at:at + 10])
 
 
+def test_logits_past_32_bits():
+    T, E, K = 2_200_000, 1024, 4                       # 4.5 GB
+    part = draw(1000, E, "bf16", 17)
+    l = part.repeat(T // 1000, 1)
+    for score, bias, groups, top in (("softmax", None, 1, 1), ("sigmoid", draw(1, E, "fp32", 18)[0], 4, 2)):
+        kw = dict(bias=bias, score=score, groups=groups, top_groups=top)
+        ids, w = M.moonep_router(l, K, **kw)
+        a, b = M.moonep_router(part, K, **kw)
+        assert torch.equal(ids.view(-1, 1000, K), a.expand(T // 1000, -1, -1))
+        assert torch.equal(w.view(-1, 1000, K), b.expand(T // 1000, -1, -1))
+        g = M.moonep_router_bwd(l, ids, w, score=score, normalize=False)
+        assert torch.equal(g[-1000:], M.moonep_router_bwd(part, a, b, score=score, normalize=False))
+        del g
+
+
 def test_captured_and_on_another_stream():
     l, g = draw(300, 256, "fp32", 14), draw(300, 8, "fp32", 15)
     b = draw(1, 256, "fp32", 16)[0] * 0.1

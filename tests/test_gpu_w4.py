@@ -283,6 +283,26 @@ def test_two_plans_on_two_streams():
         assert torch.equal(g[0][m], refs[i % 2][0][m]) and torch.equal(g[1][m], refs[i % 2][1][m])
 
 
+def test_slabs_further_apart_than_32_bits():
+    # three slabs 2.2 GB apart: the last one's offset is past 2^32
+    c = Case4(1, 3, 2, 40, 1, 128, 64, 0.5, 77)
+    need, far = c.home_w4.shape[1], 2_200_000_000 // 256 * 256
+    home, slot = (torch.empty(n, far, dtype=torch.uint8, device="cuda") for n in (3, 1))
+    el = 3 * c.H * c.I
+    wide = torch.empty(3, far // 2, dtype=torch.bfloat16, device="cuda")
+    wide[:, :el] = c.unrounded
+    M.moonep_w4_pack(wide, c.H, c.I, out=home)
+    assert torch.equal(home[:, :need], c.home_w4)
+    M.moonep_w4_unpack(home, c.H, c.I, out=wide)
+    assert torch.equal(wide[:, :el], c.home_w)
+    slot[0, :need] = c.slot_w4[0, 0]
+    x = c.rows8()
+    y = M.moonep_expert_ffn_w4(c.plan, c.recv, home, slot[None], c.I)[0]
+    y8 = M.moonep_expert_ffn_w4q8(c.plan, x, home, slot[None], c.H, c.I)[0]
+    assert torch.equal(y[c.mapped], M.moonep_expert_ffn_w4(c.plan, c.recv, c.home_w4, c.slot_w4, c.I)[0][c.mapped])
+    assert torch.equal(y8[c.mapped], M.moonep_expert_ffn_w4q8(c.plan, x, c.home_w4, c.slot_w4, c.H, c.I)[0][c.mapped])
+
+
 def test_an_invalid_plan_writes_nothing():
     ids = np.full((8, 2), 99, dtype=np.int32)
     plan = M.moonep_plan(torch.from_numpy(ids).cuda(), torch.ones(8, 2, device="cuda"), 2, 4, 2, 4, 1)
