@@ -1,6 +1,7 @@
 """MI355X-native balanced expert-parallel hot path: plan -> zero-copy dispatch ->
 weighted combine -> replica-gradient reduce, and the expert block's compute around it (the
-gated feed-forward experts and the norm in front of them, forward and backward), as HIP
+gated feed-forward experts and the norm in front of them, forward and backward, the experts with
+weights in 4 bits, and the router that makes the plan's input), as HIP
 kernels behind a C ABI (include/moonep.h, libmoonep.so), with a thin ctypes binding."""
 
 from .moonep import (moonep_query, moonep_plan, moonep_plan_noalloc, moonep_dispatch,  # noqa: F401

@@ -26,12 +26,12 @@
  *   - Return value: MOONEP_OK (0) or a negative MOONEP_E* code.  Argument errors
  *     (EINVAL, ELIMIT, EALIGN, EPLAN) are found on the host and nothing is enqueued; an
  *     EHIP from a call that launches several kernels (moonep_plan, the staged calls, the
- *     experts' forward call and rows' gradient, the norm's backward) can follow launches of
+ *     experts' forward calls and rows' gradient, the norm's backward) can follow launches of
  *     that call that were already enqueued.  Each call clears the
  *     thread's earlier HIP error before launching, so an EHIP is its own.  Data errors
  *     found on the device (an expert id outside [0, E)) are never reported by a return
  *     code: they set the plan's status word, read with moonep_plan_status; such a plan
- *     maps nothing (every dst_row is -1), dispatch and the experts' forward call and rows'
+ *     maps nothing (every dst_row is -1), dispatch and the experts' forward calls and rows'
  *     gradient then write nothing, combine writes zero rows, reduce adds nothing, and the
  *     weights' gradient is that of no rows.
  *   - Calls are thread-safe; the library has no global mutable state apart from
