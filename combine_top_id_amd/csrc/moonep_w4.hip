@@ -711,7 +711,7 @@ int check_packing(const uint16_t* w, int64_t W_el, int64_t n, int H, int I, cons
 
 // Workgroups of four waves, a block to each.
 unsigned pack_grid(int64_t blocks) { return (unsigned)std::min<int64_t>((blocks + 3) / 4, 1 << 23); }
-bool passes_cache(int64_t n, int H, int I) { return n * 6 * I * H > kLastLevelCacheBytes; }
+bool passes_cache(int64_t n, int H, int I) { return n > (int64_t)kLastLevelCacheBytes / (6ll * I * H); }
 
 template <bool Q8>
 int ffn_w4(const moonep_plan_desc* plan, const uint8_t* in, int64_t in_row, int H, int I, int act, const uint8_t* home,
