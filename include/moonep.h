@@ -461,7 +461,8 @@ int moonep_expert_tile_w4(const moonep_plan_desc* plan, int H, int I, int rows_q
  *   two largest keys; the top_groups best groups are kept (1 of 1: all experts).
  *   topk_ids  the K experts of these groups with the largest keys, largest first
  *   topk_w    scale * s of each (fp32, without the bias), divided by their sum if normalize is 1
- * Equal keys and equal group scores go to the lowest index.  Keys are compared in 64 bits.
+ * Equal keys and equal group scores go to the lowest index.  Keys are compared in 64 bits; without a bias and groups
+ * the logits are compared, which is their order.
  * A logit of -inf or NaN masks its expert: its score is 0, whatever its bias, and it is chosen only
  * where a token has fewer than K others, the lowest index first, with weight 0 (all weights are 0 for a
  * token without any); a group's score leaves it out, and is -inf if nothing else is there.  A bias of
