@@ -617,23 +617,24 @@ hipError_t launch_tiles(W4Args a, hipStream_t st) {
 // the fewest times.  An expert's group and its replicas end inside a tile: half of one to each group.
 // Measured on MI355X, us of each launch (Few, Medium, Tall; and with 8-bit rows Few, Small, Medium, Tall, Large; mean
 // rows of an expert; R 8 for 64 experts, 4 for 16, 3 for 21):
-//   64 experts, H 7168, I 2048, gate and up    1: 121, 123, 154          141, 127, 129, 133, 174
-//                                             16: 248, 262, 282          241, 243, 262, 246, 309
-//                                             64: 559, 399, 383          436, 344, 302, 280, 364
-//                                            256: 1790, 1225, 1047      1266, 844, 668, 636, 630
-//                               down          16: 129, 122, 136          128, 134, 125, 121, 142
-//                                             64: 282, 179, 185          209, 170, 163, 135, 165
-//                                            256: 928, 587, 510          640, 418, 349, 312, 315
-//   64 experts, H 2048, I 1024, gate and up    1: 23, 31, 39              26, 23, 32, 34, 50
-//                                             32: 59, 37, 62              37, 40, 42, 48, 74
-//                                             64: 94, 60, 79              60, 46, 39, 54, 82
-//                                            256: 285, 162, 179          201, 123, 102, 118, 120
-//   16 experts, H 2048, I 1024, gate and up   32: 19, 27, 28              16, 22, 23, 22, 30
-//                                            128: 46, 34, 41              33, 23, 30, 26, 38
-//                                            256: 84, 61, 65              51, 38, 33, 44, 43
-//   21 experts, H 992, I 672,   gate and up   27: 14, 17, 19              12, 14, 16, 16, 23
-//                                            110: 27, 21, 26              16, 16, 18, 19, 28
-//   64 experts, H 2048, I 1408, gate and up  768: 1182, 733, 638;   32 of H 7168, I 2048, 1024: 2339, 1525, 1369, 1061, 982
+//   64 experts, H 7168, I 2048, gate and up    1: 121, 126, 154          140, 125, 128, 140, 167
+//                                             16: 246, 259, 298          231, 241, 256, 254, 305
+//                                             64: 535, 365, 427          430, 314, 287, 282, 369
+//                                            128: 940, 647, 581          691, 442, 398, 334, 434
+//                                            256: 1723, 1126, 1014      1234, 749, 586, 654, 580
+//                               down          16: 126, 123, 141          126, 129, 123, 124, 140
+//                                             64: 272, 169, 206          204, 159, 150, 135, 166
+//                                            256: 906, 555, 489          627, 380, 317, 308, 318
+//   64 experts, H 2048, I 1024, gate and up    1: 23, 30, 38              27, 24, 32, 34, 48
+//                                             32: 56, 35, 68              39, 40, 40, 49, 71
+//                                             64: 89, 54, 85              61, 41, 39, 54, 81
+//                                            256: 267, 151, 166          194, 111, 95, 112, 111
+//   16 experts, H 2048, I 1024, gate and up   32: 20, 22, 28              17, 22, 23, 22, 30
+//                                            128: 44, 30, 37              34, 22, 29, 26, 38
+//                                            256: 81, 53, 63              54, 37, 31, 44, 42
+//   21 experts, H 992, I 672,   gate and up   27: 14, 15, 20              12, 14, 16, 16, 23
+//                                            110: 27, 19, 24              18, 16, 18, 19, 27
+//   64 experts, H 2048, I 1408, gate and up  768: 1183, 736, 647;   32 of H 7168, I 2048, 1024: 2320, 1359, 1063, 1067, 985
 template <int OP, bool Q8>
 W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
   const int quads = OP == W4_FWD1 ? (I + kQuadI - 1) / kQuadI : (H + kQuadH - 1) / kQuadH;
@@ -648,7 +649,7 @@ W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
     return tiles(256, 4) >= 8 * kCus ? W4_LARGE : W4_TALL;
   } else {
     if (mean <= 20 || tiles(16, 2) <= 3 * kCus) return W4_FEW;
-    return (!few_steps && mean >= 48) || tiles(128, 4) >= 10 * kCus ? W4_TALL : W4_MEDIUM;
+    return (!few_steps && mean >= 96) || tiles(128, 4) >= 10 * kCus ? W4_TALL : W4_MEDIUM;
   }
 }
 
