@@ -595,10 +595,11 @@ struct W4Tiles {
   using Large = W4Geometry<4, 256, 2, 3, 3, 1>;                            // 8-bit rows only
   using Tall = W4Geometry<4, 128, 2, 3, 3, 1>;
   using Medium = std::conditional_t<Q8, W4Geometry<4, 64, 1, 2, 2, 3>, W4Geometry<4, 32, 1, 2, 2, 3>>;
+  using Pair = W4Geometry<4, 64, 1, 2, 2, 2>;                              // bf16 rows only
   using Small = W4Geometry<2, 64, 2, 3, 3, 3>;                             // 8-bit rows only
   using Few = W4Geometry<2, 16, 1, 4, 2, Q8 ? 4 : 3>;
 };
-enum W4Tile { W4_LARGE, W4_TALL, W4_MEDIUM, W4_SMALL, W4_FEW };
+enum W4Tile { W4_LARGE, W4_TALL, W4_PAIR, W4_MEDIUM, W4_SMALL, W4_FEW };
 
 template <int OP, bool Q8, class G>
 hipError_t launch_tiles(W4Args a, hipStream_t st) {
@@ -615,26 +616,26 @@ hipError_t launch_tiles(W4Args a, hipStream_t st) {
 // smallest that still is about one round over the CUs, as long as the few steps of a tile are no more than its start
 // and its end, which other workgroups of the CU work beside; else the large ones, which read rows and weights
 // the fewest times.  An expert's group and its replicas end inside a tile: half of one to each group.
-// Measured on MI355X, us of each launch (Few, Medium, Tall; and with 8-bit rows Few, Small, Medium, Tall, Large; mean
+// Measured on MI355X, us of each launch (Few, Medium, Pair, Tall; and with 8-bit rows Few, Small, Medium, Tall, Large; mean
 // rows of an expert; R 8 for 64 experts, 4 for 16, 3 for 21):
-//   64 experts, H 7168, I 2048, gate and up    1: 121, 126, 154          140, 125, 128, 140, 167
-//                                             16: 246, 259, 298          231, 241, 256, 254, 305
-//                                             64: 535, 365, 427          430, 314, 287, 282, 369
-//                                            128: 940, 647, 581          691, 442, 398, 334, 434
-//                                            256: 1723, 1126, 1014      1234, 749, 586, 654, 580
-//                               down          16: 126, 123, 141          126, 129, 123, 124, 140
-//                                             64: 272, 169, 206          204, 159, 150, 135, 166
-//                                            256: 906, 555, 489          627, 380, 317, 308, 318
-//   64 experts, H 2048, I 1024, gate and up    1: 23, 30, 38              27, 24, 32, 34, 48
-//                                             32: 56, 35, 68              39, 40, 40, 49, 71
-//                                             64: 89, 54, 85              61, 41, 39, 54, 81
-//                                            256: 267, 151, 166          194, 111, 95, 112, 111
-//   16 experts, H 2048, I 1024, gate and up   32: 20, 22, 28              17, 22, 23, 22, 30
-//                                            128: 44, 30, 37              34, 22, 29, 26, 38
-//                                            256: 81, 53, 63              54, 37, 31, 44, 42
-//   21 experts, H 992, I 672,   gate and up   27: 14, 15, 20              12, 14, 16, 16, 23
-//                                            110: 27, 19, 24              18, 16, 18, 19, 27
-//   64 experts, H 2048, I 1408, gate and up  768: 1183, 736, 647;   32 of H 7168, I 2048, 1024: 2320, 1359, 1063, 1067, 985
+//   64 experts, H 7168, I 2048, gate and up    1: 121, 126, 152, 154       140, 125, 128, 140, 167
+//                                             16: 246, 259, 267, 298       231, 241, 256, 254, 305
+//                                             64: 535, 365, 319, 427       430, 314, 287, 282, 369
+//                                            128: 940, 647, 561, 581       691, 442, 398, 334, 434
+//                                            256: 1723, 1126, 1028, 1014   1234, 749, 586, 654, 580
+//                               down          16: 126, 123, 120, 141       126, 129, 123, 124, 140
+//                                             64: 272, 169, 178, 206       204, 159, 150, 135, 166
+//                                            256: 906, 555, 525, 489       627, 380, 317, 308, 318
+//   64 experts, H 2048, I 1024, gate and up    1: 23, 30, 29, 38           27, 24, 32, 34, 48
+//                                             32: 56, 35, 55, 68           39, 40, 40, 49, 71
+//                                             64: 89, 54, 64, 85           61, 41, 39, 54, 81
+//                                            256: 267, 151, 154, 166       194, 111, 95, 112, 111
+//   16 experts, H 2048, I 1024, gate and up   32: 20, 22, 32, 28           17, 22, 23, 22, 30
+//                                            128: 44, 30, 37, 37           34, 22, 29, 26, 38
+//                                            256: 81, 53, 62, 63           54, 37, 31, 44, 42
+//   21 experts, H 992, I 672,   gate and up   27: 14, 15, 20, 20           12, 14, 16, 16, 23
+//                                            110: 27, 19, 22, 24           18, 16, 18, 19, 27
+//   64 experts, H 2048, I 1408, gate and up  768: 1183, 736, 674, 647;   32 of H 7168, I 2048, 1024: 2320, 1359, 1063, 1067, 985
 template <int OP, bool Q8>
 W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
   const int quads = OP == W4_FWD1 ? (I + kQuadI - 1) / kQuadI : (H + kQuadH - 1) / kQuadH;
@@ -649,7 +650,8 @@ W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
     return tiles(256, 4) >= 8 * kCus ? W4_LARGE : W4_TALL;
   } else {
     if (mean <= 20 || tiles(16, 2) <= 3 * kCus) return W4_FEW;
-    return (!few_steps && mean >= 96) || tiles(128, 4) >= 10 * kCus ? W4_TALL : W4_MEDIUM;
+    if (!few_steps && mean >= 48) return mean < 160 ? W4_PAIR : W4_TALL;
+    return tiles(128, 4) >= 10 * kCus ? W4_TALL : W4_MEDIUM;
   }
 }
 
@@ -660,6 +662,8 @@ hipError_t launch(const W4Args& a, hipStream_t st) {
   if constexpr (Q8) {
     if (t == W4_LARGE) return launch_tiles<OP, Q8, typename T::Large>(a, st);
     if (t == W4_SMALL) return launch_tiles<OP, Q8, typename T::Small>(a, st);
+  } else {
+    if (t == W4_PAIR) return launch_tiles<OP, Q8, typename T::Pair>(a, st);
   }
   switch (t) {
     case W4_TALL: return launch_tiles<OP, Q8, typename T::Tall>(a, st);
@@ -680,6 +684,7 @@ void tile_size(const moonep_sizes& s, int H, int I, int32_t tile[2]) {
   switch (w4_tile<OP, Q8>(s, H, I)) {
     case W4_LARGE: return tile_size<Q8, typename T::Large>(tile);
     case W4_TALL: return tile_size<Q8, typename T::Tall>(tile);
+    case W4_PAIR: return tile_size<Q8, typename T::Pair>(tile);
     case W4_MEDIUM: return tile_size<Q8, typename T::Medium>(tile);
     case W4_SMALL: return tile_size<Q8, typename T::Small>(tile);
     default: return tile_size<Q8, typename T::Few>(tile);

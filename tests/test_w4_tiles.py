@@ -32,7 +32,7 @@ def test_the_tiles_are_those_that_are_meant():
 
 
 def test_every_tile_is_taken():
-    few = {(128, 16), (256, 32), (256, 128)}
+    few = {(128, 16), (256, 32), (256, 64), (256, 128)}
     for q8, all_ in ((False, few), (True, {(128, 16), (128, 64), (256, 64), (256, 128), (256, 256)})):
         for product in ("gate_up", "down"):
             assert {t for _, q, pr, t in TILES if q == q8 and pr == product} == all_
