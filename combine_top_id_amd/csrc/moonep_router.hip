@@ -290,13 +290,22 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
   const int nv = (a.E + L - 1) / L;            // 32 at most: v is five bits of a key
   uint64_t* const held64 = reinterpret_cast<uint64_t*>(smem + (plain ? 0 : (a.E + 3) / 4 * 16) + (threadIdx.x >> 6) * held_bytes(a.E, L, a.groups));
   uint32_t* const held = reinterpret_cast<uint32_t*>(held64) + lane / L * a.E;
+  // softmax: the least bias of a wave's experts that are not masked, and of all
+  __shared__ float lows[4];
+  float low = INFINITY;
   const uint32_t magic = grouped ? ((1u << 20) + a.E / a.groups - 1) / (a.E / a.groups) : 0;   // e / size for e < 1024, size <= 512
   if constexpr (!plain) {
     for (int e = threadIdx.x; e < a.E; e += 256) {
       const float b = a.bias ? a.bias[e] : 0.f;
       bias[e] = b == b ? b : -INFINITY;
+      low = fminf(low, b > -INFINITY ? b : INFINITY);
+    }
+    if constexpr (SCORE == kSoftmax) {
+      low = least<64>(low);
+      if (lane == 0) lows[threadIdx.x >> 6] = low;
     }
     __syncthreads();
+    if constexpr (SCORE == kSoftmax) low = fminf(fminf(lows[0], lows[1]), fminf(lows[2], lows[3]));
   }
   for (int64_t first = (int64_t)blockIdx.x * kTokens; first < a.T; first += (int64_t)gridDim.x * kTokens) {
     const int64_t t = min(first + mine, a.T - 1);          // the last token again, where there is none
@@ -343,8 +352,9 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
       total = sum<L>(total);
     }
     const float over_total = 1.f / total;
-    // an expert's score in fp32: off by 3 * 2^-23 (sigmoid), by 2^-17 of itself (softmax: up
-    // to 128 roundings, of the argument's size and of the sum)
+    // an expert's score in fp32: off by 3 * 2^-23 (sigmoid), by 2^-17 of itself and 2^-63 (softmax, x away from the
+    // largest logit: 52 + 2.25 x roundings, of the sum and of the argument's size, are 128 up to x = 33, and beyond
+    // it, down to where the exponential underflows, the score is below 2^-47)
     auto score32 = [&](float x) -> float {
       return SCORE == kSoftmax ? __expf(x - top) * over_total : __builtin_amdgcn_rcpf(1.f + __expf(-x));
     };
@@ -430,18 +440,21 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
       const float b = !plain && sub <= a.K && id >= 0 ? bias[id] : 0.f;
       float f = x, s = 0.f;
       if (!plain) {
-        s = score32(x);
+        s = x > -INFINITY ? score32(x) : 0.f;
         f = x > -INFINITY ? s + b : -INFINITY;
       }
       auto next = [](float v) {
         if constexpr (L == 16) return __uint_as_float(dpp<0x101>(__float_as_uint(v)));
         return __uint_as_float(dpp<0x130>(__float_as_uint(v)));
       };
-      const float fn = next(f), xn = next(x), bn = next(b);
+      const float fn = next(f), xn = next(x), bn = next(b), sn = next(s);
       const int idn = (int)__float_as_uint(next(__uint_as_float((uint32_t)id)));
       const bool last = sub == a.K - 1;
-      float gap = plain ? 0.f : fabsf(f) * 0x1p-22f + (SCORE == kSoftmax ? s * 0x1p-16f : 0x1p-20f);
-      if (last) gap += fabsf(f) * 0x1p-17f;                // others may be hidden in the five bits
+      // both keys are off, each by its own score's error.  Behind the last one others may be hidden, by the five bits or
+      // by their errors: their scores are not larger than the largest, nor than what the least bias leaves of a key
+      const float hidden = fminf(over_total, f - low + (fabsf(f) + fabsf(low)) * 0x1p-16f);
+      float gap = plain ? 0.f : fabsf(f) * 0x1p-22f + (SCORE == kSoftmax ? (s + (last ? hidden : sn)) * 0x1p-17f + 0x1p-62f : 0x1p-20f);
+      if (last) gap += fabsf(f) * 0x1p-17f;
       // masked ones are in order, and so are equal ones; what is beyond the last is not known to be
       const bool apart = f - fn > gap || (f > -INFINITY && fn == -INFINITY) || (f == -INFINITY && fn == -INFINITY && x == -INFINITY) ||
                          (!last && x == xn && b == bn && id < idn);

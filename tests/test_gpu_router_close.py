@@ -1,0 +1,79 @@
+"""The router's choice where two keys are nearly or exactly equal, or at the ends of fp32's range: what the comparison
+by short keys has to hand on to the one in 64 bits.  Ids exactly, as in tests/test_gpu_router.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_top_id_amd as M
+from tests import router_ref as R
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    M.lib()
+
+
+def same_ids(l, K, bias=None, score="softmax", groups=1, top_groups=1, normalize=True):
+    """`l` fp32 [T, E] and `bias` fp32 [E], numpy."""
+    ids, _ = M.moonep_router(torch.from_numpy(l).cuda(), K, bias=None if bias is None else torch.from_numpy(bias).cuda(),
+                             score=score, groups=groups, top_groups=top_groups, normalize=normalize)
+    ref, got = R.choose(l, bias, score, K, groups, top_groups), ids.cpu().numpy()
+    bad = np.nonzero((got != ref).any(1))[0]
+    assert not len(bad), f"{len(bad)} of {len(l)} tokens differ, token {bad[0]}: {got[bad[0]]}, not {ref[bad[0]]}"
+
+
+def rivals(score, T, E, seed):
+    """Logits and biases with pairs of experts, one with a score of 1e-6 to 1e-5 and one of about a tenth, whose keys
+    differ by 1e-10 to 1e-7 only: two experts of every eight, each pair's keys 1e-5 below the last's, all other keys far below."""
+    rng = np.random.RandomState(seed)
+    n = min(E // 4, 16) // 2                             # pairs
+    eights = rng.permutation(E // 8)[:n]
+    one, two = (np.array([rng.permutation(8)[:2] for _ in range(n)]) + 8 * eights[:, None]).T
+    level = 2e-5 + 1e-5 * np.arange(n)[::-1]
+    bias = np.full(E, -2.0, np.float32)
+    bias[one] = level - 10.0 ** rng.uniform(-6, -5, n)
+    bias[two] = level - 0.9 / n * rng.uniform(0.5, 1.0, n)
+    off = rng.randn(T, n) * 10.0 ** rng.uniform(-10, -7, (T, 1))
+    small, large = level - bias[one].astype(np.float64) + 0 * off, level - bias[two].astype(np.float64) + off
+    l = np.zeros((T, E))
+    if score == "softmax":
+        l[:] = np.log((1 - small.sum(1, keepdims=True) - large.sum(1, keepdims=True)) / (E - 2 * n))
+        l[:, one], l[:, two] = np.log(small), np.log(large)
+    else:
+        l[:, one], l[:, two] = (np.log(s) - np.log1p(-s) for s in (small, large))
+    return l.astype(np.float32), bias
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(64, 1), (64, 5), (64, 8), (256, 1), (256, 8), (256, 15), (512, 5), (256, 16), (1024, 5)])
+def test_unlike_scores_with_nearly_equal_keys(score, E, K):
+    for seed in range(4):
+        say(f"router rivals E={E} K={K} {score} seed={seed}")
+        l, b = rivals(score, 500, E, seed)
+        same_ids(l, K, b, score)
+        same_ids(l, min(K, 8), b, score, groups=8, top_groups=4, normalize=False)
+
+
+def test_a_rounded_score_behind_a_tiny_bias():
+    # key 1 is 1/25 less its rounding to fp32, which is more than 1e-30; in fp32 it is zero
+    l, b = np.zeros((1, 26), np.float32), np.full(26, -1.0, np.float32)
+    l[0, 0], b[0], b[1] = -200, 1e-30, -np.float32(1 / 25)
+    assert R.choose(l, b, "softmax", 1)[0, 0] == 1
+    same_ids(l, 1, b)
+    same_ids(np.concatenate([l, l + 3]), 2, b)
+
+
+def test_scores_below_the_smallest_normal_number():
+    rng = np.random.RandomState(5)
+    for E, K in ((64, 8), (384, 8), (1024, 16)):
+        say(f"router tiny scores E={E} K={K}")
+        l = (-86 - 20 * rng.rand(100, E)).astype(np.float32)
+        l[:, 3] = 0                                      # the others' scores are between 2^-153 and 2^-124
+        same_ids(l, K, np.zeros(E, np.float32))
+        same_ids(l, K, (rng.randint(-3, 4, E) * 2.0 ** -149).astype(np.float32))
+        same_ids(l, K, np.zeros(E, np.float32), groups=4, top_groups=2)
