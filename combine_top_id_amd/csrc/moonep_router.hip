@@ -454,7 +454,7 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
       // by their errors: their scores are not larger than the largest, nor than what the least bias leaves of a key
       const float hidden = fminf(over_total, f - low + (fabsf(f) + fabsf(low)) * 0x1p-16f);
       float gap = plain ? 0.f : fabsf(f) * 0x1p-22f + (SCORE == kSoftmax ? (s + (last ? hidden : sn)) * 0x1p-17f + 0x1p-62f : 0x1p-20f);
-      if (last) gap += fabsf(f) * 0x1p-17f;
+      if (last) gap += fabsf(f) * 0x1p-17f + 0x1p-144f;    // the five bits, of subnormal numbers too
       // masked ones are in order, and so are equal ones; what is beyond the last is not known to be
       const bool apart = f - fn > gap || (f > -INFINITY && fn == -INFINITY) || (f == -INFINITY && fn == -INFINITY && x == -INFINITY) ||
                          (!last && x == xn && b == bn && id < idn);

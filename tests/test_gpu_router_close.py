@@ -77,3 +77,22 @@ def test_scores_below_the_smallest_normal_number():
         same_ids(l, K, np.zeros(E, np.float32))
         same_ids(l, K, (rng.randint(-3, 4, E) * 2.0 ** -149).astype(np.float32))
         same_ids(l, K, np.zeros(E, np.float32), groups=4, top_groups=2)
+
+
+@pytest.mark.parametrize("E,K", [(64, 1), (64, 7), (300, 15), (600, 8), (1024, 31)])
+def test_subnormal_logits(E, K):
+    for seed, top in enumerate((25, 60, 1000, 1 << 22)):
+        say(f"router subnormal logits E={E} K={K} up to {top} units")
+        rng = np.random.RandomState(seed)
+        l = (rng.randint(-top, top + 1, (200, E)) * 2.0 ** -149).astype(np.float32)
+        same_ids(l, K)
+        same_ids(l, K, score="sigmoid", normalize=False)
+        l[rng.rand(200, E) < 0.9] = -1.0                 # few beside many that are far below
+        same_ids(l, K)
+
+
+def test_a_subnormal_logit_behind_two_smaller_ones():
+    l = np.full((1, 64), -1.0, np.float32)
+    l[0, [0, 1, 20]] = np.float32(2.0 ** -149) * np.array([3, 1, 20], np.float32)
+    assert R.choose(l, None, "softmax", 1)[0, 0] == 20
+    same_ids(l, 1)
