@@ -81,10 +81,12 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_a
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
+constexpr float kLargest = 3.402823466e38f;      // number in fp32
+
 // A logit as it counts: NaN as -inf (an expert that is masked), +inf as the largest number, -0 as 0.
 __device__ __forceinline__ float clean(float l) {
   l += 0.f;
-  return l == l ? fminf(l, 3.402823466e38f) : -INFINITY;
+  return l == l ? fminf(l, kLargest) : -INFINITY;
 }
 
 // Integers in the order of the numbers.  0 is for experts that cannot be chosen (any more), 1 for those
@@ -167,7 +169,8 @@ __device__ __forceinline__ uint64_t best_groups(const K* held, int sub, int E, i
       }
     }
     // two keys that are not masked, or as many as there are
-    score[j] = g < groups && part == 0 && (j == 0 || shift == 0) ? order(number(m1) + (m2 > masked ? number(m2) : 0)) : 0;
+    const K two = m1 > masked ? order(number(m1) + (m2 > masked ? number(m2) : 0)) : masked;
+    score[j] = g < groups && part == 0 && (j == 0 || shift == 0) ? two : 0;
   }
   uint64_t chosen = 0;
   K last = 0;
@@ -297,7 +300,7 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
   if constexpr (!plain) {
     for (int e = threadIdx.x; e < a.E; e += 256) {
       const float b = a.bias ? a.bias[e] : 0.f;
-      bias[e] = b == b ? b : -INFINITY;
+      bias[e] = b == b ? fminf(b, kLargest) : -INFINITY;   // +inf would be no number among the short keys
       low = fminf(low, b > -INFINITY ? b : INFINITY);
     }
     if constexpr (SCORE == kSoftmax) {
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
     // a score underflows to +0, so that no sum is -0
     auto key_of = [&](int v, float l) -> uint32_t {
       if constexpr (plain) return short_key(clean(l), v);
-      float x = score32(SCORE == kSoftmax ? fminf(l, 3.402823466e38f) : l);
+      float x = score32(SCORE == kSoftmax ? fminf(l, kLargest) : l);
       x += bias[v * L + sub];
       return short_key(l > -INFINITY ? x : -INFINITY, v);
     };
@@ -379,9 +382,9 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
       wave_sync();
       chosen = best_groups<L>(
           held, sub, a.E, a.groups, a.top_groups, kMasked32, [](uint32_t k) { return k > kMasked32 ? number(k) : -INFINITY; },
-          [](float x) { return x > -INFINITY ? order(x + 0.f) : kMasked32; },
-          // two keys of each, off by their errors and five bits
-          [&](float) { return (SCORE == kSoftmax ? 0x1p-14f : 0x1p-18f) + largest * 0x1p-15f; }, close);
+          [](float x) { return order(fmaxf(x, -kLargest) + 0.f); },
+          // two keys of each, off by their errors and five bits; sums that may be out of range say nothing
+          [&](float) { return largest < 0x1p126f ? (SCORE == kSoftmax ? 0x1p-14f : 0x1p-18f) + largest * 0x1p-15f : INFINITY; }, close);
     }
     uint32_t k0 = 0, k1 = 0, k2 = 0, k3 = 0;               // the lane's best four
     auto take = [&](uint32_t x) {
@@ -455,9 +458,9 @@ __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
       const float hidden = fminf(over_total, f - low + (fabsf(f) + fabsf(low)) * 0x1p-16f);
       float gap = plain ? 0.f : fabsf(f) * 0x1p-22f + (SCORE == kSoftmax ? (s + (last ? hidden : sn)) * 0x1p-17f + 0x1p-62f : 0x1p-20f);
       if (last) gap += fabsf(f) * 0x1p-17f + 0x1p-144f;    // the five bits, of subnormal numbers too
-      // masked ones are in order, and so are equal ones; what is beyond the last is not known to be
+      // masked ones are in order, and so are equal ones, but for biases that may be +inf; what is beyond the last is not known to be
       const bool apart = f - fn > gap || (f > -INFINITY && fn == -INFINITY) || (f == -INFINITY && fn == -INFINITY && x == -INFINITY) ||
-                         (!last && x == xn && b == bn && id < idn);
+                         (!last && x == xn && b == bn && b < kLargest && id < idn);
       if (sub < a.K && idn >= 0 && !apart) close = true;
     }
     // one token after another, by all lanes

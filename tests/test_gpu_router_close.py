@@ -96,3 +96,47 @@ def test_a_subnormal_logit_behind_two_smaller_ones():
     l[0, [0, 1, 20]] = np.float32(2.0 ** -149) * np.array([3, 1, 20], np.float32)
     assert R.choose(l, None, "softmax", 1)[0, 0] == 20
     same_ids(l, 1)
+
+
+MAX = float(np.finfo(np.float32).max)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_with_biases_at_the_ends_of_the_range(score):
+    for i, (T, E, K, groups, top) in enumerate([(20, 64, 6, 8, 3), (9, 256, 8, 8, 4), (7, 12, 2, 12, 2), (5, 1024, 16, 64, 8),
+                                                (11, 64, 4, 2, 1), (6, 768, 8, 3, 1)]):
+        rng = np.random.RandomState(40 + i)
+        l = rng.randn(T, E).astype(np.float32)
+        size = E // groups
+        for what, values in dict(on=[np.inf, 0, 0, 0, 0], off=[-MAX, 0], on_and_off=[np.inf, -np.inf, 0, 0, 0, 0], ends=[MAX, -MAX],
+                                 all=[np.inf, MAX, 3e38, 1.0, -1e38, -MAX, -np.inf], lowest=[-MAX, -np.inf, -3e38]).items():
+            say(f"router biases {what} E={E} groups={groups} {score}")
+            for _ in range(4):
+                b = rng.choice(np.array(values, np.float32), E)
+                same_ids(l, K, b, score, groups, top)
+                # whole groups alike
+                b = np.repeat(rng.choice(np.array(values, np.float32), groups), size)
+                same_ids(l, K, b, score, groups, top)
+        b = np.zeros(E, np.float32)
+        b[E - 2] = np.inf                                # one expert that every token takes
+        assert (R.choose(l, b, score, K, groups, top)[:, 0] == E - 2).all()
+        same_ids(l, K, b, score, groups, top)
+
+
+def test_a_group_of_lowest_biases_before_one_that_is_masked():
+    l, b = np.zeros((3, 16), np.float32), np.zeros(16, np.float32)
+    l[:, :8] = -np.inf                                   # nothing left in the first group
+    b[8:] = -MAX
+    assert (R.choose(l, b, "sigmoid", 2, 2, 1) == [8, 9]).all()
+    same_ids(l, 2, b, "sigmoid", 2, 1)
+    same_ids(l, 2, b, "softmax", 2, 1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_at_the_ends_of_the_range(score):
+    for E, K in ((64, 6), (384, 15), (700, 8)):
+        rng = np.random.RandomState(E)
+        l = rng.randint(-2, 3, (30, E)).astype(np.float32)
+        for values in ([np.inf, MAX, 3e38, 0.0], [np.inf, 0, 0, 0, 0, 0, 0], [-MAX, -np.inf, -3e38, 1.0], [np.inf, MAX, -MAX, -np.inf]):
+            say(f"router biases {values} E={E} {score}")
+            same_ids(l, K, rng.choice(np.array(values, np.float32), E), score)
