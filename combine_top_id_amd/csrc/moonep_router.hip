@@ -202,8 +202,8 @@ __host__ __device__ constexpr int held_bytes(int E, int L, int groups) {
   return (E * (tokens > 1 ? tokens * 4 : 8) + 15) / 16 * 16;
 }
 
-// A token's choice by keys in 64 bits, by a whole wave: lane k has the k-th.  Its loops are not unrolled: it is
-// needed so rarely that a wave waits for each line of its code to come from memory.
+// A token's choice by keys in 64 bits, by a whole wave: lane k has the k-th.  Its loops are not unrolled: with ordinary
+// fp32 logits it is needed so rarely that a wave waits for each line of its code to come from memory.
 template <class T, int SCORE, int MODE>
 __device__ __forceinline__ int exact_choice(const RouterArgs& a, int64_t t, uint64_t* held) {
   constexpr bool plain = MODE == kPlain;
@@ -272,14 +272,21 @@ __device__ __forceinline__ int exact_choice(const RouterArgs& a, int64_t t, uint
 
 // The choice is made in two ways.  First by keys in fp32 less five bits, of which each lane holds its best four in
 // order, so that a round is a reduction over the lanes and one move; then the K chosen and the next one are looked
-// at, and only where two of them are too close for fp32 to tell (one token in 400 of 384 experts with biases), or are
-// equal, the wave chooses again by keys in 64 bits.  Logits in bf16 without biases and groups are exact in
+// at, and only where the order of two is too close for fp32 to tell, or the last one and the next are equal, the wave
+// chooses again by keys in 64 bits, one token after another.  Logits in bf16 without biases and groups are exact in
 // the short keys.
+// These are few with normal fp32 logits of spread 1.5 (of 384 experts with biases 3 tokens in 1000 by sigmoids, 1 by
+// softmax), and many where keys tie or lie close together (131072 tokens, K 8):
+//   fp32 logits that hold bf16 values: a tenth of the tokens of 384 experts; 85 us where others of fp32 take 49
+//   groups whose scores differ by less than what is allowed for their errors, 2^-14 with softmax, 2^-18 with sigmoids: 256
+//     experts in 8 groups without biases, softmax of logits of spread 0.1: 320 us, 0.02: 481, where 1.5 is 136; sigmoids of
+//     logits below -14: 430 for 89
 //
 // 16 lanes a token rather than 64: a reduction is four moves in place of six, and a wave's four tokens share each
 // instruction.  Measured on MI355X: 131072 tokens of 384 fp32 experts with biases, K 8: 60 us, of which the vector
-// instructions are 45 (the logits' bytes would take 32); with all keys in 64 bits 386.  8 tokens of 256 experts
-// in 8 groups: 8.8, a token's chain from one step to the next (64 lanes were no faster).
+// instructions are 45 (the logits' bytes would take 32); with all keys in 64 bits 386.  The same by softmax: 85.  8 tokens
+// of 256 experts in 8 groups with biases: 8.8, and 7.6 a launch in a graph, where the same without groups and biases are 4.0
+// (64 lanes were no faster).
 template <class T, int SCORE, bool NORM, int L, int MODE>
 __global__ __launch_bounds__(256, 4) void router_kernel(const RouterArgs a) {
   constexpr bool plain = MODE == kPlain;       // the logits' order is the scores'

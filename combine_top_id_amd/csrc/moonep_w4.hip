@@ -636,6 +636,9 @@ hipError_t launch_tiles(W4Args a, hipStream_t st) {
 //   21 experts, H 992, I 672,   gate and up   27: 14, 15, 20, 20           12, 14, 16, 16, 23
 //                                            110: 27, 19, 22, 24           18, 16, 18, 19, 27
 //   64 experts, H 2048, I 1408, gate and up  768: 1183, 736, 674, 647;   32 of H 7168, I 2048, 1024: 2320, 1359, 1063, 1067, 985
+// The rule takes the best tile of these or one within 5%, but for 8-bit rows in the first product of 64 experts: with a row
+// each it takes Few (140 for 125, 27 for 24), with 16 of H 7168 Tall (254 for 231), with 256 Tall (654 for 580; of H 2048 112 for
+// 95).  Nothing was measured between 16 and 56 steps, where its limit of 32 lies.
 template <int OP, bool Q8>
 W4Tile w4_tile(const moonep_sizes& s, int H, int I) {
   const int quads = OP == W4_FWD1 ? (I + kQuadI - 1) / kQuadI : (H + kQuadH - 1) / kQuadH;

@@ -466,7 +466,8 @@ int moonep_expert_tile_w4(const moonep_plan_desc* plan, int H, int I, int rows_q
  * A logit of -inf or NaN masks its expert: its score is 0, whatever its bias, and it is chosen only
  * where a token has fewer than K others, the lowest index first, with weight 0 (all weights are 0 for a
  * token without any); a group's score leaves it out, and is -inf if nothing else is there.  A bias of
- * -inf or NaN does the same to the choice.  A logit of +inf counts as the largest fp32 number.
+ * -inf or NaN does the same to the choice, one of +inf puts its expert, and its group, first.  A logit of +inf counts as
+ * the largest fp32 number.
  *   logits    device fp32 (dtype MOONEP_F32) or bf16 (MOONEP_BF16) [T, E]
  *   bias      device fp32 [E] or NULL: moves the choice, not the weights
  *   score     MOONEP_SCORE_*          scale  finite
