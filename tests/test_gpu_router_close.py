@@ -27,14 +27,14 @@ def same_ids(l, K, bias=None, score="softmax", groups=1, top_groups=1, normalize
     assert not len(bad), f"{len(bad)} of {len(l)} tokens differ, token {bad[0]}: {got[bad[0]]}, not {ref[bad[0]]}"
 
 
-def rivals(score, T, E, seed):
+def rivals(score, T, E, seed, step=1e-5):
     """Logits and biases with pairs of experts, one with a score of 1e-6 to 1e-5 and one of about a tenth, whose keys
-    differ by 1e-10 to 1e-7 only: two experts of every eight, each pair's keys 1e-5 below the last's, all other keys far below."""
+    differ by 1e-10 to 1e-7 only: two experts of every eight, each pair's keys `step` below the last's, all other keys far below."""
     rng = np.random.RandomState(seed)
     n = min(E // 4, 16) // 2                             # pairs
     eights = rng.permutation(E // 8)[:n]
     one, two = (np.array([rng.permutation(8)[:2] for _ in range(n)]) + 8 * eights[:, None]).T
-    level = 2e-5 + 1e-5 * np.arange(n)[::-1]
+    level = 2e-5 + step * np.arange(n)[::-1]
     bias = np.full(E, -2.0, np.float32)
     bias[one] = level - 10.0 ** rng.uniform(-6, -5, n)
     bias[two] = level - 0.9 / n * rng.uniform(0.5, 1.0, n)
@@ -57,6 +57,15 @@ def test_unlike_scores_with_nearly_equal_keys(score, E, K):
         l, b = rivals(score, 500, E, seed)
         same_ids(l, K, b, score)
         same_ids(l, min(K, 8), b, score, groups=8, top_groups=4, normalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,top", [(64, 4, 8, 3), (64, 1, 8, 1), (64, 16, 8, 4), (128, 8, 16, 5), (512, 8, 64, 4), (1024, 6, 64, 3)])
+def test_groups_with_nearly_equal_sums_of_unlike_scores(score, E, K, groups, top):
+    for seed, step in enumerate((0.0, 1e-9, 1e-7, 4e-6)):
+        say(f"router sums E={E} K={K} groups={groups} top={top} {score} step={step}")
+        l, b = rivals(score, 200, E, seed, step)
+        same_ids(l, K, b, score, groups, top)
 
 
 def test_a_rounded_score_behind_a_tiny_bias():
